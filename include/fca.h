@@ -345,6 +345,178 @@ fca_status fca_paged_decode_static(const void *q, const void *k_cache, const voi
                                    void *out, float *lse, float scale, int32_t *dev_status,
                                    void *stream);
 
+/*
+ * New tokens in the cache.  The calls below put a step's new tokens into the
+ * paged cache and attend with them: prompts taken in chunks, drafted tokens
+ * to verify, decodes beside either.  They have no counterpart in the method's
+ * description; they are what a batch goes through before it is decoded with
+ * the calls above, over the same caches and block tables:
+ *
+ *   fca_extend_tables    lengths -> grown block tables, cache slots
+ *   fca_append_kv        new keys and values -> their slots
+ *   fca_chunk_plan / fca_chunk_plan_update   the step's work lists
+ *   fca_chunk_attention  one layer's attention of the new tokens
+ *
+ * Blocks hold 16 tokens.  Request r has cached_lens[r] tokens in the cache
+ * and brings new_lens[r]; the new tokens of all requests are packed in
+ * request order, request r's in rows [q_starts[r], q_starts[r + 1]).
+ * Error bits that the kernels OR into a device status word:
+ *   8    a length, or a request's range of rows, is out of range
+ *   16   a used block id or slot is out of range
+ *   64   the free list has too few blocks
+ *   128  more new tokens than slots
+ */
+
+/*
+ * fca_extend_tables -- grow the requests' block tables by blocks off a free
+ * list and give every new token its cache slot, from the requests' lengths,
+ * on the device.
+ *
+ * Request r holds ceil(cached / 16) blocks and comes to need
+ * ceil((cached + new) / 16); the new ones are taken off the list in request
+ * order, then table order.  Token i of request r sits at position
+ * p = cached + i and gets slot block_tables[r][p / 16] * 16 + p % 16.
+ *
+ *   block_tables  DEVICE int32 [num_requests][max_blocks], in and out: the new
+ *                 entries are written, the others stay as they are.
+ *   cached_lens, new_lens   DEVICE int32 [num_requests], not negative; their sum
+ *                 at most max_blocks * 16.  A request's last, partly filled
+ *                 block must be its own: new tokens are written into it.
+ *   free_blocks   DEVICE int32 [num_free]: ids in [0, num_blocks).
+ *   free_next     DEVICE int32: index in free_blocks of the first block not
+ *                 taken yet.
+ *   seq_lens      DEVICE int32 [num_requests], out: cached + new (may be
+ *                 cached_lens itself).
+ *   q_starts      DEVICE int32 [num_requests + 1], out: first row of each
+ *                 request's new tokens; the last one is their total.
+ *   slots         DEVICE int32 [num_slots], out: each new token's slot, -1
+ *                 behind the last (fca_append_kv skips those).
+ *   free_after    DEVICE int32, out: free_next plus the blocks taken (may be
+ *                 free_next itself).
+ *   dev_status    DEVICE int32, or NULL: error bits are ORed into it.
+ *
+ * All or nothing: when a length is out of range, the list has too few blocks,
+ * an id that would be used is out of range, or there are more new tokens
+ * than slots, the bit is set and no table changes: seq_lens becomes
+ * cached_lens, free_after free_next, q_starts 0 and every slot -1, so that
+ * the calls that follow have no new tokens.
+ *
+ * Returns FCA_ERR_INVALID_ARG (null or misaligned pointer, bad shape, buffers
+ * that overlap otherwise than stated, as far as seq_lens and cached_lens
+ * do), FCA_ERR_UNSUPPORTED (over 16384 requests, or
+ * num_blocks or max_blocks beyond 2^31 / 16), FCA_ERR_CUDA.  num_requests == 0
+ * sets q_starts[0] to 0, the slots to -1 and free_after.  Asynchronous on
+ * `stream`, one kernel, no workspace; runs on the current device.
+ */
+fca_status fca_extend_tables(int32_t *block_tables, int32_t max_blocks, const int32_t *cached_lens,
+                             const int32_t *new_lens, int32_t num_requests, const int32_t *free_blocks,
+                             int32_t num_free, const int32_t *free_next, int32_t num_blocks,
+                             int32_t *seq_lens, int32_t *q_starts, int32_t *slots, int32_t num_slots,
+                             int32_t *free_after, int32_t *dev_status, void *stream);
+
+/*
+ * fca_append_kv -- write new keys and values into the paged caches.
+ *
+ *   k, v     DEVICE bf16, num_tokens rows of [num_kv_heads][head_dim], 16-byte
+ *            aligned; consecutive rows are k_row_stride / v_row_stride elements
+ *            apart (a multiple of 8, at least num_kv_heads * head_dim: rows may
+ *            sit in a wider projection output).
+ *   slots    DEVICE int32 [num_tokens]: row i goes to token slots[i] % 16 of
+ *            block slots[i] / 16; a negative slot skips the row.  A slot of
+ *            num_blocks * 16 or more skips the row too and sets bit 16.  Two
+ *            rows with one slot leave either of them there.
+ *   k_cache, v_cache  DEVICE bf16 [num_blocks][16][num_kv_heads][head_dim],
+ *            16-byte aligned, not overlapping k or v.
+ *   dev_status  DEVICE int32, or NULL: error bits are ORed into it.
+ *
+ * Returns FCA_ERR_INVALID_ARG, FCA_ERR_UNSUPPORTED (head_dim not 64 or 128,
+ * num_blocks beyond 2^31 / 16), FCA_ERR_CUDA.  num_tokens == 0 is a no-op.  Asynchronous on `stream`,
+ * one kernel; runs on the current device.
+ */
+fca_status fca_append_kv(const void *k, int64_t k_row_stride, const void *v, int64_t v_row_stride,
+                         const int32_t *slots, int32_t num_tokens, int32_t num_blocks,
+                         int32_t num_kv_heads, int32_t head_dim, void *k_cache, void *v_cache,
+                         int32_t *dev_status, void *stream);
+
+/* Opaque plan of one step's chunk attention: copies of the tables and lengths,
+ * the work lists and the workspace of fca_chunk_attention.  Library-owned;
+ * free with fca_chunk_plan_destroy.  Serves every layer of the step; kept for
+ * the next step by fca_chunk_plan_update. */
+typedef struct fca_chunk_plan_s *fca_chunk_plan_t;
+
+/* fca_chunk_plan flag: every row sees all seq_len tokens (cross attention to an
+ * encoder's states in the cache), instead of those up to its own position. */
+#define FCA_CHUNK_FULL 1u
+
+/*
+ * fca_chunk_plan -- the work lists for rows of new tokens over the paged cache.
+ *
+ *   block_tables  DEVICE int32 [num_requests][max_blocks]; entries at
+ *                 j >= ceil(seq_len / 16) are ignored.
+ *   seq_lens      DEVICE int32 [num_requests]: tokens in the cache, the chunk's
+ *                 own included (append first); at most max_blocks * 16, and at
+ *                 least the request's rows unless FCA_CHUNK_FULL.
+ *   q_starts      DEVICE int32 [num_requests + 1]: starts at 0, does not
+ *                 decrease, ends at most at num_tokens.  A request may have no
+ *                 rows.
+ *   num_tokens    rows in the buffers that fca_chunk_attention gets.  Rows
+ *                 behind q_starts[num_requests] are not touched.
+ *   block_size 16, num_blocks, num_q_heads, num_kv_heads, head_dim as fca_plan.
+ *   flags         0 or FCA_CHUNK_FULL.
+ *   out_plan      HOST, out: the new plan (NULL on error).
+ *
+ * Allocates from the library's plan pool, runs on `stream` and synchronises it
+ * once.  The inputs may be reused once it returns.  Errors as fca_plan
+ * (FCA_ERR_INVALID_ARG: shapes, lengths or q_starts out of range).
+ */
+fca_status fca_chunk_plan(const int32_t *block_tables, int32_t max_blocks, const int32_t *seq_lens,
+                          const int32_t *q_starts, int32_t num_requests, int32_t num_tokens,
+                          int32_t block_size, int32_t num_blocks, int32_t num_q_heads,
+                          int32_t num_kv_heads, int32_t head_dim, uint32_t flags,
+                          fca_chunk_plan_t *out_plan, void *stream);
+
+/*
+ * fca_chunk_plan_update -- the plan for another step of the same shape:
+ * other tables, lengths and rows, the same num_requests, max_blocks and
+ * num_tokens (pad with requests of no rows).  Asynchronous on `stream`, two kernels, no
+ * allocation, so it can be captured in a graph with the attention; the inputs must stay
+ * valid until `stream` has run it, and updates and attentions of one plan
+ * must be ordered.  What fca_chunk_plan would refuse sets an error bit in the plan's
+ * device status instead (fca_chunk_check_status): with bad q_starts no row
+ * is written; a request with a bad length or block id gets out 0 and lse -inf.
+ */
+fca_status fca_chunk_plan_update(fca_chunk_plan_t plan, const int32_t *block_tables, int32_t max_blocks,
+                                 const int32_t *seq_lens, const int32_t *q_starts, int32_t num_requests,
+                                 void *stream);
+
+/*
+ * fca_chunk_attention -- softmax attention of the plan's rows over the paged
+ * cache, one layer.  Row i of a request with n rows and seq_len L is at
+ * position p = L - n + i and sees tokens 0..p (with FCA_CHUNK_FULL: all L).  What a
+ * row does not see has no part in it, whatever it holds (inf and NaN included).
+ * A row that sees nothing gets out 0 and lse -inf.
+ *
+ *   q        DEVICE bf16, num_tokens rows of [num_q_heads][head_dim], 16-byte
+ *            aligned, q_row_stride elements apart (a multiple of 8, at least
+ *            num_q_heads * head_dim).
+ *   k_cache, v_cache, scale  as fca_decode.
+ *   out      DEVICE bf16 [num_tokens][num_q_heads][head_dim], 16-byte aligned; not
+ *            overlapping q.
+ *   lse      DEVICE fp32 [num_tokens][num_q_heads], or NULL.
+ *
+ * Asynchronous on `stream`.  Uses the plan's workspace: attentions that share
+ * a plan must be ordered.  The result of a row does not depend on timing: the same call on
+ * the same inputs gives the same bits.
+ */
+fca_status fca_chunk_attention(const void *q, int64_t q_row_stride, const void *k_cache, const void *v_cache,
+                               fca_chunk_plan_t plan, void *out, float *lse, float scale, void *stream);
+
+/* Read and clear the plan's device error word, as fca_check_device_status. */
+fca_status fca_chunk_check_status(fca_chunk_plan_t plan, void *stream, int32_t *code);
+
+/* Free a chunk plan (synchronises the device first).  NULL is ok. */
+fca_status fca_chunk_plan_destroy(fca_chunk_plan_t plan);
+
 /* Text of the last CUDA error a call of this library met on the calling
  * thread ("no error" if none); valid until the next failing call. */
 const char *fca_last_cuda_error(void);

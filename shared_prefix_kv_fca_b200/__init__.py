@@ -14,6 +14,14 @@ The method ("ZoRRo Inference & Forest Cascade Attention", "Core Mechanism"):
 group discovery over the requests' block tables, one grouped pass per group
 over its shared prefix blocks, one pass per request over its own blocks, and
 a log-sum-exp weighted merge; equal to standard attention.
+
+New tokens get into the same caches, and attend, by
+
+    fca_extend_tables(block_tables, cached_lens, new_lens, free_blocks, free_next,
+                      num_blocks, seq_lens, q_starts, slots)
+    fca_append_kv(k, v, slots, k_cache, v_cache, num_blocks)
+    plan = fca_chunk_plan(block_tables, seq_lens, q_starts, T, num_blocks, Hq, Hkv, D)
+    fca_chunk_attention(q, k_cache, v_cache, plan, out, lse, scale)
 """
 from __future__ import annotations
 
@@ -29,6 +37,8 @@ __all__ = [
     "fca_status_string", "fca_version", "fca_plan_opts_default", "library_path", "load_library",
     "fca_prefix_pass", "fca_suffix_pass", "fca_merge_pass", "fca_last_cuda_error",
     "FCA_PLAN_FLAT", "FCA_PLAN_ASYNC_UPDATE", "STATUS", "fca_paged_decode_static", "FCA_STATIC_SCRATCH_BYTES",
+    "ChunkPlan", "fca_extend_tables", "fca_append_kv", "fca_chunk_plan", "fca_chunk_plan_update", "fca_chunk_attention",
+    "fca_chunk_check_status", "fca_chunk_plan_destroy", "FCA_CHUNK_FULL",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -37,6 +47,7 @@ _lib = None
 
 FCA_PLAN_FLAT = 1
 FCA_PLAN_ASYNC_UPDATE = 2
+FCA_CHUNK_FULL = 1
 STATUS = {0: "FCA_OK", 1: "FCA_ERR_INVALID_ARG", 2: "FCA_ERR_BAD_BLOCK_ID", 3: "FCA_ERR_UNSUPPORTED",
           4: "FCA_ERR_CUDA", 5: "FCA_ERR_OOM", 6: "FCA_ERR_DEVICE_FLAG", 7: "FCA_ERR_TOO_LARGE"}
 FCA_STATIC_SCRATCH_BYTES = 64 << 20
@@ -117,6 +128,22 @@ def load_library():
     lib.fca_paged_decode_static.argtypes = [vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, vp, vp, f32,
                                             vp, vp]
     lib.fca_paged_decode_static.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    lib.fca_extend_tables.argtypes = [vp, i32, vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, i32, vp, vp, vp]
+    lib.fca_extend_tables.restype = ctypes.c_int
+    lib.fca_append_kv.argtypes = [vp, i64, vp, i64, vp, i32, i32, i32, i32, vp, vp, vp, vp]
+    lib.fca_append_kv.restype = ctypes.c_int
+    lib.fca_chunk_plan.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, i32, ctypes.c_uint32,
+                                   ctypes.POINTER(vp), vp]
+    lib.fca_chunk_plan.restype = ctypes.c_int
+    lib.fca_chunk_plan_update.argtypes = [vp, vp, i32, vp, vp, i32, vp]
+    lib.fca_chunk_plan_update.restype = ctypes.c_int
+    lib.fca_chunk_attention.argtypes = [vp, i64, vp, vp, vp, vp, vp, f32, vp]
+    lib.fca_chunk_attention.restype = ctypes.c_int
+    lib.fca_chunk_check_status.argtypes = [vp, vp, i32p]
+    lib.fca_chunk_check_status.restype = ctypes.c_int
+    lib.fca_chunk_plan_destroy.argtypes = [vp]
+    lib.fca_chunk_plan_destroy.restype = ctypes.c_int
     lib.fca_status_string.argtypes = [ctypes.c_int]
     lib.fca_status_string.restype = ctypes.c_char_p
     lib.fca_version.argtypes = []
@@ -324,6 +351,162 @@ def fca_paged_decode_static(q, k_cache, v_cache, block_tables, seq_lens, num_blo
     _check(rc, "fca_paged_decode_static")
 
 
+def _check_ints(t, name: str, shape=None, least: int = 0) -> None:
+    if not t.is_cuda or str(t.dtype) != "torch.int32" or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.numel() < least:
+        raise ValueError(f"{name} must have at least {least} element(s)")
+
+
+def _check_rows(t, name: str, shape) -> int:
+    """A bf16 tensor [rows, heads, D] whose rows are contiguous but may be
+    apart (views of a wider projection output); returns the row stride."""
+    if not t.is_cuda or str(t.dtype) != "torch.bfloat16":
+        raise ValueError(f"{name} must be a bf16 CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    rows, heads, D = shape
+    packed = heads * D
+    if rows <= 1:                   # a single row's stride says nothing
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: each row of {heads} heads must be contiguous")
+        return packed
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: each row of {heads} heads must be contiguous")
+    if t.stride(0) < packed or t.stride(0) % 8:
+        raise ValueError(f"{name}: rows must be a multiple of 8 elements apart, at least {packed}, not {t.stride(0)}")
+    return int(t.stride(0))
+
+
+def fca_extend_tables(block_tables, cached_lens, new_lens, free_blocks, free_next, num_blocks: int, seq_lens,
+                      q_starts, slots, free_after=None, dev_status=None, stream=None) -> None:
+    """Grow block_tables [R, max_blocks] by blocks off free_blocks for new_lens
+    [R] more tokens than cached_lens [R], and write seq_lens [R], q_starts
+    [R + 1], the new tokens' cache slots (-1 behind the last) and the list
+    position free_after.  seq_lens may be cached_lens; free_after None
+    updates free_next in place.  All int32 CUDA tensors.  A step that cannot be
+    made is refused whole on the device: error bits in dev_status (an int32
+    tensor of one element, or None), no table changed, no new tokens."""
+    lib = load_library()
+    _check_ints(block_tables, "block_tables")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [R, max_blocks]")
+    R, mb = block_tables.shape
+    _check_ints(cached_lens, "cached_lens", (R,))
+    _check_ints(new_lens, "new_lens", (R,))
+    _check_ints(seq_lens, "seq_lens", (R,))
+    _check_ints(q_starts, "q_starts", (R + 1,))
+    for t, name in ((free_blocks, "free_blocks"), (slots, "slots")):
+        _check_ints(t, name)
+        if t.dim() != 1:
+            raise ValueError(f"{name} must have one dimension")
+    _check_ints(free_next, "free_next", least=1)
+    free_after = free_next if free_after is None else free_after
+    _check_ints(free_after, "free_after", least=1)
+    if dev_status is not None:
+        _check_ints(dev_status, "dev_status", least=1)
+    dev = _one_device(("block_tables", block_tables), ("cached_lens", cached_lens), ("new_lens", new_lens),
+                      ("free_blocks", free_blocks), ("free_next", free_next), ("seq_lens", seq_lens),
+                      ("q_starts", q_starts), ("slots", slots), ("free_after", free_after),
+                      ("dev_status", dev_status))
+    with _on_device(dev):
+        rc = lib.fca_extend_tables(_ptr(block_tables), mb, _ptr(cached_lens), _ptr(new_lens), R, _ptr(free_blocks),
+                                   free_blocks.numel(), _ptr(free_next), num_blocks, _ptr(seq_lens), _ptr(q_starts),
+                                   _ptr(slots), slots.numel(), _ptr(free_after), _ptr(dev_status),
+                                   _stream_handle(stream, dev))
+    _check(rc, "fca_extend_tables")
+
+
+def fca_append_kv(k, v, slots, k_cache, v_cache, num_blocks: int, dev_status=None, stream=None) -> None:
+    """Write rows of k and v (bf16 [T, Hkv, D], rows may be strided) to slots
+    [T] (int32; negative: skip) of the caches.  A slot out of range skips its
+    row and sets bit 16 of dev_status (an int32 tensor of one element, or None)."""
+    lib = load_library()
+    if k.dim() != 3:
+        raise ValueError(f"k must be [T, Hkv, D], not {tuple(k.shape)}")
+    T, Hkv, D = k.shape
+    ks = _check_rows(k, "k", (T, Hkv, D))
+    vs = _check_rows(v, "v", (T, Hkv, D))
+    _check_ints(slots, "slots", (T,))
+    _check_caches(k_cache, v_cache, num_blocks, Hkv, D)
+    if dev_status is not None:
+        _check_ints(dev_status, "dev_status", least=1)
+    dev = _one_device(("k", k), ("v", v), ("slots", slots), ("k_cache", k_cache), ("v_cache", v_cache),
+                      ("dev_status", dev_status))
+    with _on_device(dev):
+        rc = lib.fca_append_kv(_ptr(k), ks, _ptr(v), vs, _ptr(slots), T, num_blocks, Hkv, D, _ptr(k_cache),
+                               _ptr(v_cache), _ptr(dev_status), _stream_handle(stream, dev))
+    _check(rc, "fca_append_kv")
+
+
+def _check_chunk_tables(block_tables, seq_lens, q_starts) -> None:
+    _check_tables(block_tables, seq_lens)
+    _check_ints(q_starts, "q_starts", (seq_lens.shape[0] + 1,))
+
+
+def fca_chunk_plan(block_tables, seq_lens, q_starts, num_tokens: int, num_blocks: int, num_q_heads: int,
+                   num_kv_heads: int, head_dim: int, block_size: int = 16, full: bool = False,
+                   stream=None) -> "ChunkPlan":
+    """Work lists of one step's chunk attention: request r's rows are
+    [q_starts[r], q_starts[r + 1]) of num_tokens, its cache holds seq_lens[r]
+    tokens (the chunk's own included).  full: every row sees all of them.
+    Serves every layer of the step."""
+    lib = load_library()
+    _check_chunk_tables(block_tables, seq_lens, q_starts)
+    dev = _one_device(("block_tables", block_tables), ("seq_lens", seq_lens), ("q_starts", q_starts))
+    R, mb = block_tables.shape
+    handle = ctypes.c_void_p()
+    with _on_device(dev):       # the plan belongs to the device current when it is built
+        rc = lib.fca_chunk_plan(_ptr(block_tables), mb, _ptr(seq_lens), _ptr(q_starts), R, num_tokens, block_size,
+                                num_blocks, num_q_heads, num_kv_heads, head_dim, FCA_CHUNK_FULL if full else 0,
+                                ctypes.byref(handle), _stream_handle(stream, dev))
+    _check(rc, "fca_chunk_plan")
+    return ChunkPlan(handle, R, num_tokens, num_q_heads, num_kv_heads, head_dim, full, num_blocks, dev)
+
+
+def fca_chunk_plan_update(plan: "ChunkPlan", block_tables, seq_lens, q_starts, stream=None) -> None:
+    """The plan for another step of the same shape, without synchronising the
+    host (the C call of the same name)."""
+    _check_chunk_tables(block_tables, seq_lens, q_starts)
+    _plan_device(plan, ("block_tables", block_tables), ("seq_lens", seq_lens), ("q_starts", q_starts))
+    R, mb = block_tables.shape
+    _check(load_library().fca_chunk_plan_update(plan.handle, _ptr(block_tables), mb, _ptr(seq_lens), _ptr(q_starts), R,
+                                                _stream_handle(stream, plan.device)), "fca_chunk_plan_update")
+
+
+def fca_chunk_attention(q, k_cache, v_cache, plan: "ChunkPlan", out, lse=None, scale=None, stream=None) -> None:
+    """Attention of the plan's rows q (bf16 [T, Hq, D], rows may be strided)
+    over the paged caches into out (bf16 [T, Hq, D]) and lse (fp32 [T, Hq])."""
+    lib = load_library()
+    if scale is None:
+        scale = 1.0 / math.sqrt(plan.head_dim)
+    shape = (plan.num_tokens, plan.num_q_heads, plan.head_dim)
+    stride = _check_rows(q, "q", shape)
+    _check_bf16(out, "out", shape)
+    _check_caches(k_cache, v_cache, plan.num_blocks, plan.num_kv_heads, plan.head_dim)
+    _check_lse(lse, plan.num_tokens, plan.num_q_heads)
+    _plan_device(plan, ("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("out", out), ("lse", lse))
+    _check(lib.fca_chunk_attention(_ptr(q), stride, _ptr(k_cache), _ptr(v_cache), plan.handle, _ptr(out), _ptr(lse),
+                                   float(scale), _stream_handle(stream, plan.device)), "fca_chunk_attention")
+
+
+def fca_chunk_check_status(plan: "ChunkPlan", stream=None) -> int:
+    """Raw device error word of a chunk plan (0 = fine); raises FcaError when it is set."""
+    code = ctypes.c_int32()
+    rc = load_library().fca_chunk_check_status(plan.handle, _stream_handle(stream, plan.device), ctypes.byref(code))
+    if rc not in (0, 6):
+        _check(rc, "fca_chunk_check_status")
+    if rc == 6:
+        raise FcaError(rc, f"fca_chunk_check_status (word {code.value:#x})")
+    return int(code.value)
+
+
+def fca_chunk_plan_destroy(plan: "ChunkPlan") -> None:
+    plan.close()
+
+
 def _check_pass_inputs(q, k_cache, v_cache, plan: "Plan") -> None:
     _check_bf16(q, "q", (plan.num_requests, plan.num_q_heads, plan.head_dim))
     _check_caches(k_cache, v_cache, plan.num_blocks, plan.num_kv_heads, plan.head_dim)
@@ -453,6 +636,40 @@ class Plan:
     def close(self) -> None:
         if self.handle is not None and self.handle.value:
             _check(load_library().fca_plan_destroy(self.handle), "fca_plan_destroy")
+        self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+class ChunkPlan:
+    """Owner of an fca_chunk_plan_t handle."""
+
+    def __init__(self, handle: ctypes.c_void_p, R: int, T: int, Hq: int, Hkv: int, D: int, full: bool,
+                 num_blocks: int, device: Optional[int] = None):
+        self.handle = handle
+        self.num_requests, self.num_tokens = R, T
+        self.num_q_heads, self.num_kv_heads, self.head_dim = Hq, Hkv, D
+        self.full = full
+        self.num_blocks = num_blocks
+        self.device = device        # CUDA device index the plan belongs to
+
+    def update(self, block_tables, seq_lens, q_starts, stream=None) -> None:
+        """Another step of the same shape (fca_chunk_plan_update)."""
+        fca_chunk_plan_update(self, block_tables, seq_lens, q_starts, stream)
+
+    def close(self) -> None:
+        if self.handle is not None and self.handle.value:
+            _check(load_library().fca_chunk_plan_destroy(self.handle), "fca_chunk_plan_destroy")
         self.handle = None
 
     def __del__(self):

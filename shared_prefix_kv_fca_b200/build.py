@@ -18,8 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libfca_b200.so")
 SOURCES = ["fca_api.cu", "fca_plan.cu", "fca_suffix.cu", "fca_prefix.cu", "fca_merge.cu", "fca_static.cu",
-           "fca_selftest.cu"]
-HEADERS = ["fca_internal.h", "fca_device.cuh"]
+           "fca_selftest.cu", "fca_tables.cu", "fca_append.cu", "fca_chunk_plan.cu", "fca_chunk.cu"]
+HEADERS = ["fca_internal.h", "fca_device.cuh", "fca_chunk.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -65,20 +65,6 @@ bool make_cache_map(CUtensorMap* map, const void* base, int32_t num_blocks, int3
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Makes a plan's device current for one call and restores the caller's
-// device afterwards (a no-op when it is current already).
-struct DeviceGuard {
-    int prev = -1;
-    explicit DeviceGuard(int dev) {
-        int cur = 0;
-        if (cudaGetDevice(&cur) == cudaSuccess && cur != dev && cudaSetDevice(dev) == cudaSuccess) prev = cur;
-        (void)cudaGetLastError();
-    }
-    ~DeviceGuard() {
-        if (prev >= 0) cudaSetDevice(prev);
-    }
-};
-
 }  // namespace fca
 
 using namespace fca;

@@ -31,6 +31,11 @@ constexpr int32_t kErrUpdateRefused = 32;  // an asynchronous fca_plan_update wa
 constexpr int32_t kErrStaticSeqLen = 8;    // seq_len outside [1, max_blocks * block_size]
 constexpr int32_t kErrStaticBlockId = 16;  // a used table entry outside [0, num_blocks)
 
+// The calls for new tokens (fca_extend_tables, fca_append_kv, fca_chunk_*)
+// share the two bits above and add these.
+constexpr int32_t kErrNoBlocks = 64;       // the free list has too few blocks
+constexpr int32_t kErrNoSlots = 128;       // more new tokens than slots
+
 // Size of the fixed device array behind fca_paged_decode_static.
 constexpr size_t kStaticScratchBytes = size_t(64) << 20;
 
@@ -111,6 +116,23 @@ cudaError_t note_cuda(cudaError_t e);
 
 // TMA descriptor of a K or V cache [num_blocks * 16][Hkv][D] bf16 (fca_api.cu).
 bool make_cache_map(CUtensorMap* map, const void* base, int32_t num_blocks, int32_t Hkv, int32_t D);
+
+// The memory pool plans allocate from, on the current device (fca_plan.cu).
+cudaError_t plan_pool(cudaMemPool_t* out);
+
+// Makes a plan's device current for one call and restores the caller's
+// device afterwards (a no-op when it is current already).
+struct DeviceGuard {
+    int prev = -1;
+    explicit DeviceGuard(int dev) {
+        int cur = 0;
+        if (cudaGetDevice(&cur) == cudaSuccess && cur != dev && cudaSetDevice(dev) == cudaSuccess) prev = cur;
+        (void)cudaGetLastError();
+    }
+    ~DeviceGuard() {
+        if (prev >= 0) cudaSetDevice(prev);
+    }
+};
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

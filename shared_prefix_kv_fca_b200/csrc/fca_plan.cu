@@ -919,6 +919,8 @@ __global__ void __launch_bounds__(1024) k_update_own(UpdateOwnArgs A) {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
+}  // namespace
+
 // The memory pool plans allocate from, one per device, created on first use.
 // Its release threshold is unbounded: memory a destroyed plan gave back stays
 // mapped in the pool for the next plan instead of being unmapped at the next
@@ -951,6 +953,8 @@ cudaError_t plan_pool(cudaMemPool_t* out) {
     *out = pools[dev];
     return cudaSuccess;
 }
+
+namespace {
 
 // Lays arrays out back to back (256-byte aligned) in one allocation from the
 // library's plan pool: add() records where each array goes, commit() makes
