@@ -1,9 +1,36 @@
-// fca_chunk_attention: the rows of new tokens over the paged cache.
+// fca_chunk_attention: the rows of new tokens over the paged cache, on the
+// 5th-generation tensor cores (tcgen05, accumulators in tensor memory).
 //
 // Row (token t of request r, query head h) at position p = L - n + i:
 //   s_j = scale q.k_j,  o = sum_{j <= p} exp(s_j - m) v_j / sum_j exp(s_j - m),
 //   lse = m + log sum_j exp(s_j - m)
-// over the cached tokens j that the row sees (all L of them in full plans).
+// over the cached tokens j that the row sees (all L of them in full plans), in one pass
+// over the tokens with a running reference m and running sums.
+//
+// The rows of a request that read one KV head (tokens x query heads of the
+// group) are stacked, so that a K or V stage in shared memory serves them
+// all.  A CTA walks its items of the plan (fca_chunk_plan.cu); an item is up to
+// 256 stacked rows against a range of tokens, 128 tokens a stage:
+//   - above 128 rows: two MMA tiles of 128 rows share every stage, each with its
+//     own scores, weights and accumulator, so that the softmax of one tile runs
+//     while the tensor core works for the other;
+//   - up to 128 rows: one tile's rows, but its even and odd stages go to the two
+//     halves of the machinery, whose two accumulators are joined at the end: few rows are bound by
+//     the cache's bytes, and the softmax of a stage (a row is one thread) takes
+//     longer than its bytes.
+//
+// 512 threads:
+//   warps 0-3, 4-7  softmax of tile 0 and tile 1, one thread a row: scores are
+//                read from tensor memory, the weights go back as bf16 over
+//                them, the accumulator is rescaled in place in the rare case that
+//                a row's maximum outgrows its reference;
+//   warps 8-11   query loads and epilogue;
+//   warps 12, 13 TMA loads of K and V, one block of 16 tokens a box;
+//   warps 14, 15 MMA issue, one thread each: S = Q K^T (operands in shared
+//                memory) and O += P V (P from tensor memory).
+// Every wait is bounded (fca_device.cuh); a role that gives up sets the CTA's
+// abort flag, the others leave at their next wait, copies and MMAs in flight
+// are waited for, and tensor memory is freed.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -14,30 +41,180 @@
 namespace fca {
 namespace {
 
+constexpr int kStage = kChunkStage;
+constexpr int kBlkPerStage = kStage / kBlockSize;
+constexpr int kThreads = 512;
+constexpr int kEpiWarp0 = 8;
+constexpr int kKWarp = 12, kVWarp = 13, kQKWarp = 14;   // (15: P V)
+// Registers a thread: the four warpgroups' shares add up to the launch's 128 each.
+constexpr int kRegsSoftmax = 184, kRegsEpilogue = 88, kRegsOthers = 56;
+static_assert(2 * kRegsSoftmax + kRegsEpilogue + kRegsOthers == 4 * 128, "register shares");
+// A row's exponentials use a reference that trails its running maximum: it is
+// moved (and the accumulator rescaled, a stage later) once the maximum is 2^8
+// above it, and at once, with the stage computed again, at 2^64.  Weights up to
+// 2^64 are exact powers away from their true size, well inside bf16 and fp32.
+constexpr float kRescaleLog2 = 8.f;
+constexpr float kRedoLog2 = 64.f;
+constexpr float kLn2 = 0.69314718055994531f;
+
 struct ChunkArgs {
     const ChunkItem* items;
     const int32_t* begin;
     const int32_t* end;
     const int32_t* bad;
     const int32_t* bt;
-    const int32_t* seq;
-    const int32_t* qs;
     const __nv_bfloat16* q;
     int64_t q_stride;
     const __nv_bfloat16* k;
     const __nv_bfloat16* v;
     __nv_bfloat16* out;
     float* lse;
-    int32_t R, max_blocks, num_blocks, Hq, Hkv, G, full;
+    float* part_o;
+    float* part_w;
+    float* part_lse;
+    int32_t part_rows, max_blocks, num_blocks, Hq, Hkv, G;
     float scale_log2;
     int32_t* err;
 };
 
-// One row by one warp: a pass over its tokens with the running maximum and
-// sum, lane i holding D / 32 of the row's elements.
 template <int D>
-__device__ void exact_row(const ChunkArgs& a, int32_t req, int32_t head, const __nv_bfloat16* q, int32_t tok0, int32_t tok1,
-                          float (&o)[D / 32], float& m, float& l) {
+struct Layout {
+    static constexpr int kHalves = D / 64;               // 128-byte swizzle atoms a row
+    static constexpr int kTileQ = 128 * D * 2;
+    static constexpr int kKV = kStage * D * 2;           // one K or V stage
+    static constexpr int kSlots = D == 128 ? 2 : 4;      // of K, and of V
+    static constexpr int kOffQ = 0;                      // two tiles
+    static constexpr int kOffK = kOffQ + 2 * kTileQ;
+    static constexpr int kOffV = kOffK + kSlots * kKV;
+    static constexpr int kOffML = kOffV + kSlots * kKV;  // [2][3][128] f32: row reference, sum, sum of rounded
+    static constexpr int kOffBar = kOffML + 2 * 3 * 128 * 4;
+    static constexpr int kNumBars = 4 * kSlots + 2 + 7 * 2 + 1;
+    static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+    static constexpr int kBytes = kOffMisc + 32;
+    static constexpr int kAlloc = kBytes + 1024;         // the operands want 1024-byte alignment
+    static constexpr uint32_t kColS = 0;                 // tile t's scores: 128 fp32 columns at 128 t
+    static constexpr uint32_t kColO = 256;               // tile t's accumulator: D columns at 256 + D t
+    static constexpr uint32_t kTmemCols = 512;
+    static_assert(kColO + 2 * D <= kTmemCols, "tensor memory budget");
+    static_assert(kAlloc <= 227 * 1024, "shared memory budget");
+};
+
+// An item and what every role derives from it.
+struct Work {
+    ChunkItem it;
+    int32_t ns;         // stages
+    int32_t ns0, ns1;   // stages of tile 0 and 1
+    bool dual;          // one tile of rows, stages dealt out to both
+};
+
+__device__ __forceinline__ int32_t row_limit(const ChunkItem& it, int32_t row, int32_t G) {
+    return min(it.tok1, it.lim0 + (it.row0 + row) / G + 1);
+}
+
+__device__ __forceinline__ Work load_work(const ChunkArgs& a, int32_t i) {
+    const int4* p = reinterpret_cast<const int4*>(a.items + i);
+    const int4 x = __ldg(p), y = __ldg(p + 1), z = __ldg(p + 2);
+    Work w;
+    w.it.req = x.x;
+    w.it.head = x.y;
+    w.it.q0 = x.z;
+    w.it.row0 = x.w;
+    w.it.nrows = y.x;
+    w.it.tok0 = y.y;
+    w.it.tok1 = y.z;
+    w.it.lim0 = y.w;
+    w.it.slot = z.x;
+    if (__ldg(a.bad + x.x)) w.it.tok1 = w.it.tok0;       // a refused request sees nothing
+    w.ns = (w.it.tok1 - w.it.tok0 + kStage - 1) / kStage;
+    w.dual = w.it.nrows <= 128;
+    if (w.dual) {
+        w.ns0 = (w.ns + 1) / 2;
+        w.ns1 = w.ns / 2;
+    } else {
+        // tile 1 holds the item's last row and has all its stages
+        w.ns0 = (max(0, row_limit(w.it, 127, a.G) - w.it.tok0) + kStage - 1) / kStage;
+        w.ns1 = w.ns;
+    }
+    return w;
+}
+
+// Byte offset of 16-byte chunk c (< 8) of row r in 64-element atom `atom` of
+// a K-major, 128-byte swizzled tile of 128 rows.
+__device__ __forceinline__ uint32_t sw128_off(int r, int atom, int c) {
+    return atom * (128 * 128) + (r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Maximum of a row's scores (raw q.k) in columns below nv.
+template <bool MASK>
+__device__ __forceinline__ float row_max(uint32_t s_addr, int nv) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kStage; c += 32) {
+        uint32_t r[32];
+        dev::tmem_ld32(s_addr + c, r);
+        dev::tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const float x = (!MASK || c + i < nv) ? __uint_as_float(r[i]) : -INFINITY;
+            const float y = (!MASK || c + i + 1 < nv) ? __uint_as_float(r[i + 1]) : -INFINITY;
+            mx = dev::max3(mx, x, y);
+        }
+    }
+    return mx;
+}
+
+// Weights of a row's stage against the reference m (log2 domain): bf16 pairs
+// in pw, their sum in sr and, for the lse, the sum before rounding in se.
+// Returns the maximum of the raw scores.
+template <bool MASK, bool LSE>
+__device__ __forceinline__ float row_weights(uint32_t s_addr, int nv, float scale_log2, float m, uint32_t (&pw)[kStage / 2],
+                                             float& se, float& sr) {
+    float2 e = make_float2(0.f, 0.f), q = make_float2(0.f, 0.f);
+    float mx = -INFINITY;
+    const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-m, -m);
+#pragma unroll
+    for (int c = 0; c < kStage; c += 64) {
+        uint32_t r0[32], r1[32];
+        dev::tmem_ld32(s_addr + c, r0);
+        dev::tmem_ld32(s_addr + c + 32, r1);
+        dev::tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+            float x = __uint_as_float(i < 32 ? r0[i & 31] : r1[i & 31]);
+            float y = __uint_as_float(i < 32 ? r0[(i + 1) & 31] : r1[(i + 1) & 31]);
+            if (MASK) {
+                x = c + i < nv ? x : -INFINITY;
+                y = c + i + 1 < nv ? y : -INFINITY;
+            }
+            mx = dev::max3(mx, x, y);
+            const float2 z = dev::fma2(make_float2(x, y), sc, nm);
+            const float2 p = make_float2(dev::ex2(z.x), dev::ex2(z.y));
+            const uint32_t w = dev::pack_bf16x2(p.x, p.y);
+            pw[(c + i) / 2] = w;
+            if (LSE) e = dev::add2(e, p);
+            q = dev::add2(q, make_float2(dev::bf16_lo(w), dev::bf16_hi(w)));
+        }
+    }
+    se = e.x + e.y;
+    sr = q.x + q.y;
+    return mx;
+}
+
+// One row by one warp with plain arithmetic, lane i holding D / 32 of the
+// row's elements: o unnormalised, against the row's maximum m, and the sum l.
+template <int D>
+__device__ __noinline__ void exact_row(const ChunkArgs& a, int32_t req, int32_t head, const __nv_bfloat16* q, int32_t tok0,
+                                       int32_t tok1, float (&o)[D / 32], float& m, float& l) {
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
     float qf[E];
@@ -58,7 +235,7 @@ __device__ void exact_row(const ChunkArgs& a, int32_t req, int32_t head, const _
         for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
         s *= a.scale_log2;
         const float top = fmaxf(m, s);
-        const float f = top == -INFINITY ? 1.f : exp2f(m - top), p = top == -INFINITY ? 0.f : exp2f(s - top);
+        const float f = top == -INFINITY ? 1.f : exp2f(m - top), p = top == -INFINITY ? exp2f(s) : exp2f(s - top);
         m = top;
         l = l * f + p;
 #pragma unroll
@@ -66,26 +243,592 @@ __device__ void exact_row(const ChunkArgs& a, int32_t req, int32_t head, const _
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(256) k_chunk_rows(ChunkArgs a) {
-    const int32_t t = blockIdx.x, head = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (head >= a.Hq || t >= a.qs[a.R]) return;
-    int32_t lo = 0, hi = a.R - 1;
-    while (lo < hi) {
-        const int32_t mid = (lo + hi + 1) >> 1;
-        if (a.qs[mid] <= t)
-            lo = mid;
-        else
-            hi = mid - 1;
+template <int D, bool LSE>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_chunk(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
+            const __grid_constant__ CUtensorMap tmV) {
+    using L = Layout<D>;
+    constexpr int NS = L::kSlots;
+    const int32_t first = a.begin[blockIdx.x], last = a.end[blockIdx.x];
+    if (first >= last) return;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+    uint64_t* k_full = bars;                // [NS] a K slot holds its stage
+    uint64_t* k_empty = k_full + NS;        // [NS] the products reading it have completed
+    uint64_t* v_full = k_empty + NS;        // [NS]
+    uint64_t* v_empty = v_full + NS;        // [NS]
+    uint64_t* q_full = v_empty + NS;        // the item's queries are written
+    uint64_t* q_free = q_full + 1;          // the item's last Q K^T has completed
+    uint64_t* s_full = q_free + 1;          // [2] a stage's scores are in the tile's columns
+    uint64_t* p_full = s_full + 2;          // [2] its weights are written over them
+    uint64_t* pv_done = p_full + 2;         // [2] the P V reading them has completed
+    uint64_t* o_full = pv_done + 2;         // [2] an item's last P V of the tile has completed
+    uint64_t* o_free = o_full + 2;          // [2] the epilogue has read the accumulator
+    uint64_t* ml_full = o_free + 2;         // [2] the tile's row state is written
+    uint64_t* ml_free = ml_full + 2;        // [2] ... and read
+    uint64_t* mma_done = ml_free + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 16);
+    float* ml = reinterpret_cast<float*>(smem + L::kOffML);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            dev::mbar_init(&k_full[s], 1);
+            dev::mbar_init(&k_empty[s], 1);
+            dev::mbar_init(&v_full[s], 1);
+            dev::mbar_init(&v_empty[s], 1);
+        }
+        dev::mbar_init(q_full, 128);
+        dev::mbar_init(q_free, 1);
+        for (int t = 0; t < 2; ++t) {
+            dev::mbar_init(&s_full[t], 1);
+            dev::mbar_init(&p_full[t], 128);
+            dev::mbar_init(&pv_done[t], 1);
+            dev::mbar_init(&o_full[t], 1);
+            dev::mbar_init(&o_free[t], 128);
+            dev::mbar_init(&ml_full[t], 128);
+            dev::mbar_init(&ml_free[t], 128);
+        }
+        dev::mbar_init(mma_done, 2);
+        *abort_flag = 0;
+        dev::fence_mbarrier_init();
     }
-    const int32_t n = a.qs[lo + 1] - a.qs[lo], L = a.bad[lo] ? 0 : a.seq[lo];
-    const int32_t seen = (a.full || L == 0) ? L : L - n + (t - a.qs[lo]) + 1;
-    float o[D / 32], m, l;
-    exact_row<D>(a, lo, head / a.G, a.q + t * a.q_stride + (int64_t)head * D, 0, seen, o, m, l);
+    if (warp == kQKWarp) {
+        dev::tmem_alloc(tmem_slot, L::kTmemCols);
+        dev::tmem_relinquish();
+    }
+    dev::tc_fence_before();
+    __syncthreads();
+    dev::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp < kEpiWarp0) {
+        // ------------------------------------------------ softmax
+        // m_ref is the reference of new exponentials; the accumulator and the
+        // sums are relative to m_used, which follows a stage later.
+        regs_inc<kRegsSoftmax>();
+        const int t = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        const uint32_t s_addr = tmem + lane_base + L::kColS + t * 128, o_addr = tmem + lane_base + L::kColO + t * D;
+        bool ok = true;
+        uint32_t g = 0;                 // stages of this tile so far
+        uint32_t gv = 0;                // stages of the CTA before the item
+        uint32_t n_items = 0;           // items with stages for this tile so far
+        Work nxt = load_work(a, first);
+        for (int32_t i = first; ok && i < last; ++i) {
+            const Work w = nxt;
+            if (i + 1 < last) nxt = load_work(a, i + 1);
+            const int32_t ns = t ? w.ns1 : w.ns0;
+            if (ns == 0) {
+                gv += w.ns;
+                continue;
+            }
+            const int r_item = w.dual ? row : t * 128 + row;             // stacked row within the item
+            const bool live = (w.dual ? quarter * 32 : t * 128 + quarter * 32) < w.it.nrows;
+            const int32_t lim = row_limit(w.it, min(r_item, w.it.nrows - 1), a.G) - w.it.tok0;   // tokens of the item it sees
+            float m_ref = -INFINITY, m_used = -INFINITY, l_exact = 0.f, l_round = 0.f;
+            for (int32_t x = 0; x < ns; ++x, ++g) {
+                const int32_t j = w.dual ? 2 * x + t : x;
+                bool got = dev::mbar_wait(&s_full[t], g & 1, abort_flag, a.err);
+                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                dev::tc_fence_after();
+                // (the scores were issued after the tile's last P V completed: the accumulator is up to date)
+                if (live) {
+                    const int nv = min(kStage, max(0, lim - j * kStage));
+                    const bool mask = __any_sync(0xffffffffu, nv < kStage);
+                    float o_scale = 1.f;
+                    if (m_used != m_ref) {                       // a move owed by the previous stage
+                        o_scale = dev::ex2(m_used - m_ref);
+                        l_exact *= o_scale;
+                        l_round *= o_scale;
+                        m_used = m_ref;
+                    }
+                    if (__any_sync(0xffffffffu, m_ref == -INFINITY)) {   // rows that have seen nothing yet
+                        const float mx = mask ? row_max<true>(s_addr, nv) : row_max<false>(s_addr, nv);
+                        if (m_ref == -INFINITY) m_ref = m_used = mx * a.scale_log2;
+                    }
+                    uint32_t pw[kStage / 2];
+                    float se = 0.f, sr = 0.f;
+#pragma unroll 1
+                    for (int attempt = 0;; ++attempt) {
+                        const float m0 = m_ref == -INFINITY ? 0.f : m_ref;      // nothing seen: every weight is 2^-inf
+                        const float mx = (mask ? row_weights<true, LSE>(s_addr, nv, a.scale_log2, m0, pw, se, sr)
+                                               : row_weights<false, LSE>(s_addr, nv, a.scale_log2, m0, pw, se, sr)) *
+                                         a.scale_log2;           // the scale is positive
+                        const bool redo = attempt == 0 && mx > m_ref + kRedoLog2;
+                        if (__any_sync(0xffffffffu, redo)) {
+                            if (redo) {
+                                const float f = dev::ex2(m_ref - mx);
+                                l_exact *= f;
+                                l_round *= f;
+                                o_scale *= f;
+                                m_ref = m_used = mx;
+                            }
+                            continue;
+                        }
+                        if (mx > m_ref + kRescaleLog2) m_ref = mx;      // moved at the next stage
+                        break;
+                    }
+                    l_exact += se;
+                    l_round += sr;
+                    if (__any_sync(0xffffffffu, o_scale != 1.f)) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t ov[16];
+                            dev::tmem_ld16(o_addr + c * 16, ov);
+                            dev::tc_wait_ld();
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-        a.out[((int64_t)t * a.Hq + head) * D + lane * (D / 32) + i] = __float2bfloat16(seen ? o[i] / l : 0.f);
-    if (a.lse && lane == 0) a.lse[(int64_t)t * a.Hq + head] = seen ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * o_scale);
+                            dev::tmem_st16(o_addr + c * 16, ov);
+                        }
+                    }
+                    uint32_t p0[32], p1[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        p0[e] = pw[e];
+                        p1[e] = pw[32 + e];
+                    }
+                    dev::tmem_st32(s_addr, p0);
+                    dev::tmem_st32(s_addr + 32, p1);
+                }
+                if (j == w.ns - 1 && (w.dual || t == 1) && w.it.tok1 % kBlockSize) {
+                    // The last block's slots behind the range were loaded too and may
+                    // hold anything, NaN included: their weights are 0, but 0 x NaN is
+                    // not, so V's rows there are cleared.
+                    const uint32_t s = (gv + j) % NS;
+                    got = dev::mbar_wait(&v_full[s], ((gv + j) / NS) & 1, abort_flag, a.err);
+                    if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                    const int r0 = w.it.tok1 - w.it.tok0 - j * kStage, r1 = (r0 + kBlockSize - 1) / kBlockSize * kBlockSize;
+                    uint8_t* vs = smem + L::kOffV + s * L::kKV;
+                    for (int e = row; e < (r1 - r0) * 8 * L::kHalves; e += 128) {
+                        const int rr = r0 + e / (8 * L::kHalves), c = e % (8 * L::kHalves);
+                        *reinterpret_cast<uint4*>(vs + sw128_off(rr, c >> 3, c & 7)) = make_uint4(0, 0, 0, 0);
+                    }
+                    dev::fence_proxy_async_smem();
+                }
+                dev::tc_wait_st();
+                dev::tc_fence_before();
+                dev::mbar_arrive(&p_full[t]);
+            }
+            if (!ok) break;
+            gv += w.ns;
+            // the rows' state for the epilogue, once it has read the last one
+            if (n_items >= 1) {
+                bool got = dev::mbar_wait(&ml_free[t], (n_items - 1) & 1, abort_flag, a.err);
+                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+            }
+            ml[t * 384 + row] = m_used;
+            ml[t * 384 + 128 + row] = l_round;
+            if (LSE) ml[t * 384 + 256 + row] = l_exact;
+            dev::mbar_arrive(&ml_full[t]);
+            ++n_items;
+        }
+    } else if (warp < kKWarp) {
+        // ------------------------------------------------ query loads and epilogue
+        regs_dec<kRegsEpilogue>();
+        const int quarter = warp & 3, tid = threadIdx.x - kEpiWarp0 * 32, row = quarter * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+        const uint32_t q_smem = dev::smem_u32(smem + L::kOffQ);
+        auto load_q = [&](const Work& w) {
+            constexpr int C = D / 8;            // 16-byte chunks a row
+            const int rows = w.dual ? 128 : 256;
+#pragma unroll 4
+            for (int e = tid; e < rows * C; e += 128) {
+                const int r = e / C, c = e % C;
+                const int32_t sr = w.it.row0 + min(r, w.it.nrows - 1);
+                const __nv_bfloat16* src =
+                    a.q + (int64_t)(w.it.q0 + sr / a.G) * a.q_stride + (w.it.head * a.G + sr % a.G) * D + c * 8;
+                cp_async16(q_smem + (r >> 7) * L::kTileQ + sw128_off(r & 127, c >> 3, c & 7), src, r < w.it.nrows ? 16u : 0u);
+            }
+            cp_async_wait();
+            dev::fence_proxy_async_smem();
+            dev::mbar_arrive(q_full);
+        };
+        // Rows of the item that this warp's threads hold in tile t: out and lse,
+        // or the piece's partial rows, from coefficients c0, c1 of the two accumulators.
+        bool ok = true;
+        uint32_t n_act = 0, n0 = 0, n1 = 0;     // items with stages; with stages for tile 0, tile 1
+        int32_t qi = first;
+        Work qw;
+        for (; qi < last; ++qi) {
+            qw = load_work(a, qi);
+            if (qw.ns) break;
+        }
+        if (qi < last) load_q(qw);
+        for (int32_t i = first; ok && i < last; ++i) {
+            const Work w = load_work(a, i);
+            if (w.ns) {
+                for (qi = i + 1; qi < last; ++qi) {
+                    qw = load_work(a, qi);
+                    if (qw.ns) break;
+                }
+                if (qi < last) {
+                    bool got = dev::mbar_wait(q_free, n_act & 1, abort_flag, a.err);
+                    if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                    load_q(qw);
+                }
+                ++n_act;
+            }
+            for (int t = 0; t < (w.dual ? 1 : 2); ++t) {
+                // the tiles whose accumulators make up these rows
+                const bool use0 = t == 0 && w.ns0 > 0, use1 = (t == 1 || w.dual) && w.ns1 > 0;
+                float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, e0 = 0.f, e1 = 0.f;
+                bool got = true;
+                if (use0) {
+                    got = dev::mbar_wait(&ml_full[0], n0 & 1, abort_flag, a.err);
+                    m0 = ml[row];
+                    l0 = ml[128 + row];
+                    if (LSE) e0 = ml[256 + row];
+                    dev::mbar_arrive(&ml_free[0]);
+                    got = got && dev::mbar_wait(&o_full[0], n0 & 1, abort_flag, a.err);
+                    ++n0;
+                }
+                if (use1) {
+                    got = got && dev::mbar_wait(&ml_full[1], n1 & 1, abort_flag, a.err);
+                    m1 = ml[384 + row];
+                    l1 = ml[384 + 128 + row];
+                    if (LSE) e1 = ml[384 + 256 + row];
+                    dev::mbar_arrive(&ml_free[1]);
+                    got = got && dev::mbar_wait(&o_full[1], n1 & 1, abort_flag, a.err);
+                    ++n1;
+                }
+                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                dev::tc_fence_after();
+                const int r_item = t * 128 + row;
+                const bool mine = r_item < w.it.nrows;
+                const float M = fmaxf(m0, m1), Mf = M == -INFINITY ? 0.f : M;
+                const float f0 = dev::ex2(m0 - Mf), f1 = dev::ex2(m1 - Mf);
+                const float l = l0 * f0 + l1 * f1, inv = l == 0.f ? 0.f : 1.f / l;
+                const float c0 = f0 * inv, c1 = f1 * inv;
+                const int32_t sr = w.it.row0 + r_item;
+                const int64_t orow = (int64_t)(w.it.q0 + sr / a.G) * a.Hq + w.it.head * a.G + sr % a.G;
+                const int64_t prow = (int64_t)w.it.slot * a.part_rows + r_item;
+                float* const po = a.part_o + prow * D;
+                __nv_bfloat16* const bo = a.out + orow * D;
+                const bool whole = w.it.slot < 0;
+                float finite = 0.f;             // NaN once an element is not finite
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float v[32];
+                    uint32_t x[32];
+                    if (use0) {
+                        dev::tmem_ld32(tmem + lane_base + L::kColO + c, x);
+                        dev::tc_wait_ld();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = use0 ? __uint_as_float(x[e]) * c0 : 0.f;
+                    if (use1) {
+                        dev::tmem_ld32(tmem + lane_base + L::kColO + D + c, x);
+                        dev::tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(x[e]), c1, v[e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) finite = fmaf(v[e], 0.f, finite);
+                    if (mine) {
+                        if (whole) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8)
+                                *reinterpret_cast<uint4*>(bo + c + e) =
+                                    make_uint4(dev::pack_bf16x2(v[e], v[e + 1]), dev::pack_bf16x2(v[e + 2], v[e + 3]),
+                                               dev::pack_bf16x2(v[e + 4], v[e + 5]), dev::pack_bf16x2(v[e + 6], v[e + 7]));
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                *reinterpret_cast<float4*>(po + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        }
+                    }
+                }
+                if (use0 || use1) {
+                    dev::tc_fence_before();
+                    if (use0) dev::mbar_arrive(&o_free[0]);
+                    if (use1) dev::mbar_arrive(&o_free[1]);
+                }
+                const float le = LSE ? M + log2f(e0 * f0 + e1 * f1) : 0.f;      // -inf for a row that saw nothing
+                if (mine) {
+                    if (!whole) {
+                        a.part_w[prow] = M + log2f(l);
+                        if (LSE) a.part_lse[prow] = le;
+                    } else if (LSE) {
+                        a.lse[orow] = le * kLn2;
+                    }
+                }
+                // A product of weight 0 with an inf or NaN that the row does not see
+                // (a later token's) is NaN: rows that are not finite are computed
+                // again from the tokens that they do see.
+                uint32_t again = __ballot_sync(0xffffffffu, mine && isnan(finite));
+                while (again) {
+                    const int src = __ffs(again) - 1;
+                    again &= again - 1;
+                    const int ri = t * 128 + quarter * 32 + src;
+                    const int64_t r_out = __shfl_sync(0xffffffffu, orow, src), r_part = __shfl_sync(0xffffffffu, prow, src);
+                    const int32_t s2 = w.it.row0 + ri;
+                    float o[D / 32], m, ls;
+                    exact_row<D>(a, w.it.req, w.it.head,
+                                 a.q + (int64_t)(w.it.q0 + s2 / a.G) * a.q_stride + (w.it.head * a.G + s2 % a.G) * D,
+                                 w.it.tok0, row_limit(w.it, ri, a.G), o, m, ls);
+                    const float scale = ls == 0.f ? 0.f : 1.f / ls;
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) {
+                        const int col = lane * (D / 32) + e;
+                        if (whole)
+                            a.out[r_out * D + col] = __float2bfloat16(o[e] * scale);
+                        else
+                            a.part_o[r_part * D + col] = o[e] * scale;
+                    }
+                    const float lw = m + log2f(ls);
+                    if (lane == 0) {
+                        if (!whole) {
+                            a.part_w[r_part] = lw;
+                            if (LSE) a.part_lse[r_part] = lw;
+                        } else if (LSE) {
+                            a.lse[r_out] = lw * kLn2;
+                        }
+                    }
+                }
+            }
+        }
+    } else {
+        regs_dec<kRegsOthers>();
+        if (warp == kKWarp || warp == kVWarp) {
+            // -------------------------------------------- TMA loads
+            // Stage g of the CTA goes to slot g % NS of its ring.  Block ids are
+            // read 32 at a time (four stages), a batch ahead.
+            const bool is_k = warp == kKWarp;
+            const CUtensorMap* tm = is_k ? &tmK : &tmV;
+            uint64_t* full = is_k ? k_full : v_full;
+            uint64_t* empty = is_k ? k_empty : v_empty;
+            uint8_t* const ring = smem + (is_k ? L::kOffK : L::kOffV);
+            if (lane == 0) dev::tma_prefetch_desc(tm);
+            constexpr int kStagesPerBatch = 32 / kBlkPerStage;
+            auto fetch = [&](const Work& w, int32_t batch) -> int32_t {
+                const int32_t blk = w.it.tok0 / kBlockSize + batch * 32 + lane;
+                // past the range: rows beyond the cache, which TMA fills with zeros
+                return blk * kBlockSize < w.it.tok1 ? __ldg(a.bt + (int64_t)w.it.req * a.max_blocks + blk) * kBlockSize
+                                                    : a.num_blocks * kBlockSize;
+            };
+            uint32_t g = 0;
+            bool ok = true;
+            Work nw = load_work(a, first);
+            int32_t nxt = fetch(nw, 0);
+            for (int32_t i = first; ok && i < last; ++i) {
+                const Work w = nw;
+                int32_t cur = nxt;
+                if (i + 1 < last) {
+                    nw = load_work(a, i + 1);
+                    nxt = fetch(nw, 0);             // the next item's first batch, while this one streams
+                }
+                int32_t more = w.ns > kStagesPerBatch ? fetch(w, 1) : 0;
+                for (int32_t j = 0; j < w.ns; ++j, ++g) {
+                    if (j && j % kStagesPerBatch == 0) {
+                        cur = more;
+                        const int32_t batch = j / kStagesPerBatch + 1;
+                        if (batch * kStagesPerBatch < w.ns) more = fetch(w, batch);
+                    }
+                    // lane e < 8 issues the boxes of the stage's block e
+                    const int32_t trow = __shfl_sync(0xffffffffu, cur, (j % kStagesPerBatch) * kBlkPerStage + (lane & 7));
+                    const uint32_t s = g % NS;
+                    if (lane == 0) {
+                        if (g >= NS && !dev::mbar_wait(&empty[s], ((g / NS) - 1) & 1, abort_flag, a.err))
+                            ok = false;
+                        else
+                            dev::mbar_arrive_expect_tx(&full[s], L::kKV);
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    if (lane < kBlkPerStage) {
+                        uint8_t* dst = ring + s * L::kKV + lane * (kBlockSize * 128);
+#pragma unroll
+                        for (int hf = 0; hf < L::kHalves; ++hf)
+                            dev::tma_load_3d(dst + hf * (kStage * 128), tm, &full[s], hf * 64, w.it.head, trow);
+                    }
+                }
+            }
+            if (lane == 0) {
+                // never leave with copies in flight (each slot's latest load only)
+                volatile int never = 0;
+                for (uint32_t j = g; j > 0 && j + NS > g; --j)
+                    dev::mbar_wait(&full[(j - 1) % NS], ((j - 1) / NS) & 1, &never, a.err);
+            }
+        } else if (lane == 0) {
+            // -------------------------------------------- MMA issue
+            bool ok = true;
+            uint32_t g = 0;                 // stages of the CTA so far
+            uint32_t c[2] = {0, 0};         // ... of each tile
+            uint32_t n_act = 0, n_tile[2] = {0, 0};
+            Work nxt = load_work(a, first);
+            for (int32_t i = first; ok && i < last; ++i) {
+                const Work w = nxt;
+                if (i + 1 < last) nxt = load_work(a, i + 1);
+                if (w.ns == 0) continue;
+                if (warp == kQKWarp) {
+                    constexpr uint32_t idesc = dev::idesc_bf16_f32(128, kStage, false, false);
+                    ok = dev::mbar_wait(q_full, n_act & 1, abort_flag, a.err);
+                    ++n_act;
+                    for (int32_t j = 0; ok && j < w.ns; ++j, ++g) {
+                        const uint32_t s = g % NS;
+                        if (!dev::mbar_wait(&k_full[s], (g / NS) & 1, abort_flag, a.err)) { ok = false; break; }
+                        const uint32_t k_base = dev::smem_u32(smem + L::kOffK) + s * L::kKV;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (w.dual ? (j & 1) != t : (t == 0 && j >= w.ns0)) continue;
+                            // the weights that lie over the tile's scores have been used
+                            if (c[t] >= 1 && !dev::mbar_wait(&pv_done[t], (c[t] - 1) & 1, abort_flag, a.err)) {
+                                ok = false;
+                                break;
+                            }
+                            dev::tc_fence_after();
+                            const uint32_t q_base = dev::smem_u32(smem + L::kOffQ) + (w.dual ? 0 : t) * L::kTileQ;
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint64_t ad = dev::smem_desc_sw128(q_base + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024);
+                                const uint64_t bd = dev::smem_desc_sw128(k_base + (k >> 2) * (kStage * 128) + (k & 3) * 32, 16, 1024);
+                                dev::tc_mma_ss(tmem + L::kColS + t * 128, ad, bd, idesc, k > 0 ? 1u : 0u);
+                            }
+                            dev::tc_commit(&s_full[t]);
+                            ++c[t];
+                        }
+                        if (!ok) break;
+                        dev::tc_commit(&k_empty[s]);
+                        if (j + 1 == w.ns) dev::tc_commit(q_free);
+                    }
+                } else {
+                    constexpr uint32_t idesc = dev::idesc_bf16_f32(128, D, false, true);
+                    const bool tail = w.it.tok1 % kBlockSize != 0;
+                    for (int32_t j = 0; ok && j < w.ns; ++j, ++g) {
+                        const uint32_t s = g % NS;
+                        if (!dev::mbar_wait(&v_full[s], (g / NS) & 1, abort_flag, a.err)) { ok = false; break; }
+                        // the tile-1 warps clear the last stage's tail for both tiles
+                        if (tail && !w.dual && j + 1 == w.ns && !dev::mbar_wait(&p_full[1], c[1] & 1, abort_flag, a.err)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t v_base = dev::smem_u32(smem + L::kOffV) + s * L::kKV;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (w.dual ? (j & 1) != t : (t == 0 && j >= w.ns0)) continue;
+                            const int32_t x = w.dual ? j >> 1 : j, ns_t = t ? w.ns1 : w.ns0;
+                            // a new item's accumulator starts once the epilogue has read the last one's
+                            if (x == 0 && n_tile[t] >= 1 &&
+                                !dev::mbar_wait(&o_free[t], (n_tile[t] - 1) & 1, abort_flag, a.err)) {
+                                ok = false;
+                                break;
+                            }
+                            if (!dev::mbar_wait(&p_full[t], c[t] & 1, abort_flag, a.err)) { ok = false; break; }
+                            dev::tc_fence_after();
+#pragma unroll
+                            for (int k = 0; k < kStage / 16; ++k) {
+                                const uint64_t bd = dev::smem_desc_sw128(v_base + k * (16 * 128), kStage * 128, 1024);
+                                dev::tc_mma_ts(tmem + L::kColO + t * D, tmem + L::kColS + t * 128 + k * 8, bd, idesc,
+                                               (x == 0 && k == 0) ? 0u : 1u);
+                            }
+                            dev::tc_commit(&pv_done[t]);
+                            if (x + 1 == ns_t) {
+                                dev::tc_commit(&o_full[t]);
+                                ++n_tile[t];
+                            }
+                            ++c[t];
+                        }
+                        if (!ok) break;
+                        dev::tc_commit(&v_empty[s]);
+                    }
+                }
+            }
+            // every MMA of this thread has retired before tensor memory is freed
+            dev::tc_commit(mma_done);
+            volatile int never = 0;
+            dev::mbar_wait(mma_done, 0, &never, a.err);
+        }
+        __syncwarp();
+    }
+
+    dev::tc_fence_before();
+    __syncthreads();
+    if (warp == kQKWarp) {
+        dev::tc_fence_after();
+        dev::tmem_dealloc(tmem, L::kTmemCols);
+    }
+}
+
+// The pieces of a cut tile joined by their weights: a warp a row.
+constexpr int kMergeThreads = 256, kMergeSplit = 4;     // CTAs a tile
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) k_chunk_merge(ChunkArgs a, const ChunkCut* cuts) {
+    constexpr int E = D / 32;
+    const ChunkCut cut = cuts[blockIdx.x];
+    const int lane = threadIdx.x & 31, pieces = cut.cta1 - cut.cta0 + 1;
+    for (int32_t row = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); row < cut.nrows;
+         row += kMergeSplit * (kMergeThreads / 32)) {
+        auto at = [&](int p) { return (int64_t)(2 * (cut.cta0 + p) + (p == 0 ? 1 : 0)) * a.part_rows + row; };
+        float M = -INFINITY, Ml = -INFINITY;
+        for (int p = lane; p < pieces; p += 32) {
+            M = fmaxf(M, a.part_w[at(p)]);
+            if (a.lse) Ml = fmaxf(Ml, a.part_lse[at(p)]);
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) {
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+            Ml = fmaxf(Ml, __shfl_xor_sync(0xffffffffu, Ml, x));
+        }
+        if (M == -INFINITY) M = 0.f;
+        if (Ml == -INFINITY) Ml = 0.f;
+        float o[E], sum = 0.f, sl = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+        for (int base = 0; base < pieces; base += 32) {
+            const int p = base + lane;
+            const float f = p < pieces ? dev::ex2(a.part_w[at(p)] - M) : 0.f;
+            if (a.lse && p < pieces) sl += dev::ex2(a.part_lse[at(p)] - Ml);
+            const int n = min(32, pieces - base);
+            for (int y = 0; y < n; ++y) {
+                const float fy = __shfl_sync(0xffffffffu, f, y);
+                const float* src = a.part_o + at(base + y) * D + lane * E;
+                sum += fy;
+                if constexpr (E == 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(src);
+                    o[0] = fmaf(fy, v.x, o[0]);
+                    o[1] = fmaf(fy, v.y, o[1]);
+                    o[2] = fmaf(fy, v.z, o[2]);
+                    o[3] = fmaf(fy, v.w, o[3]);
+                } else {
+                    const float2 v = *reinterpret_cast<const float2*>(src);
+                    o[0] = fmaf(fy, v.x, o[0]);
+                    o[1] = fmaf(fy, v.y, o[1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) sl += __shfl_xor_sync(0xffffffffu, sl, x);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int32_t sr = cut.row0 + row;
+        const int64_t orow = (int64_t)(cut.q0 + sr / a.G) * a.Hq + cut.head * a.G + sr % a.G;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + lane * E);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) dst[e / 2] = dev::pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+        if (a.lse && lane == 0) a.lse[orow] = (Ml + log2f(sl)) * kLn2;
+    }
+}
+
+template <int D, bool LSE>
+cudaError_t launch_chunk(const ChunkArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t stream) {
+    using L = Layout<D>;
+    // setmaxnreg hands out what the block was launched with: it has to have been 128 a thread
+    static const cudaError_t ready = [] {
+        cudaFuncAttributes at{};
+        cudaError_t e = cudaFuncGetAttributes(&at, k_chunk<D, LSE>);
+        if (e == cudaSuccess && at.numRegs != 128) e = cudaErrorInvalidConfiguration;
+        return e;
+    }();
+    if (ready != cudaSuccess) return ready;
+    cudaError_t e = cudaFuncSetAttribute(k_chunk<D, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    if (e != cudaSuccess) return e;
+    k_chunk<D, LSE><<<ctas, kThreads, L::kAlloc, stream>>>(a, tk, tv);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -104,33 +847,46 @@ extern "C" fca_status fca_chunk_attention(const void* q, int64_t q_row_stride, c
     if (plan->T == 0) return FCA_OK;
     DeviceGuard dg(plan->device);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CUtensorMap tk, tv;
+    if (!make_cache_map(&tk, k_cache, plan->num_blocks, plan->Hkv, plan->D) ||
+        !make_cache_map(&tv, v_cache, plan->num_blocks, plan->Hkv, plan->D))
+        return FCA_ERR_CUDA;
     ChunkArgs a;
     a.items = plan->items;
     a.begin = plan->begin;
     a.end = plan->end;
     a.bad = plan->bad;
     a.bt = plan->bt;
-    a.seq = plan->seq;
-    a.qs = plan->qs;
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.q_stride = q_row_stride;
     a.k = static_cast<const __nv_bfloat16*>(k_cache);
     a.v = static_cast<const __nv_bfloat16*>(v_cache);
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
-    a.R = plan->R;
+    a.part_o = plan->part_o;
+    a.part_w = plan->part_w;
+    a.part_lse = plan->part_lse;
+    a.part_rows = plan->part_rows;
     a.max_blocks = plan->max_blocks;
     a.num_blocks = plan->num_blocks;
     a.Hq = plan->Hq;
     a.Hkv = plan->Hkv;
     a.G = plan->G;
-    a.full = plan->full;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = plan->dev_status;
-    const dim3 grid(plan->T, (plan->Hq + 7) / 8);
+    cudaError_t e;
     if (plan->D == 128)
-        k_chunk_rows<128><<<grid, 256, 0, s>>>(a);
+        e = lse ? launch_chunk<128, true>(a, tk, tv, plan->ctas, s) : launch_chunk<128, false>(a, tk, tv, plan->ctas, s);
     else
-        k_chunk_rows<64><<<grid, 256, 0, s>>>(a);
-    return note_cuda(cudaGetLastError()) == cudaSuccess ? FCA_OK : FCA_ERR_CUDA;
+        e = lse ? launch_chunk<64, true>(a, tk, tv, plan->ctas, s) : launch_chunk<64, false>(a, tk, tv, plan->ctas, s);
+    if (note_cuda(e) != cudaSuccess) return FCA_ERR_CUDA;
+    if (plan->may_cut) {
+        const dim3 grid(plan->ctas, kMergeSplit);
+        if (plan->D == 128)
+            k_chunk_merge<128><<<grid, kMergeThreads, 0, s>>>(a, plan->cuts);
+        else
+            k_chunk_merge<64><<<grid, kMergeThreads, 0, s>>>(a, plan->cuts);
+        if (note_cuda(cudaGetLastError()) != cudaSuccess) return FCA_ERR_CUDA;
+    }
+    return FCA_OK;
 }
