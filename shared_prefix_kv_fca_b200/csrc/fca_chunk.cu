@@ -20,14 +20,22 @@
 //     longer than its bytes.
 //
 // 512 threads:
-//   warps 0-3, 4-7  softmax of tile 0 and tile 1, one thread a row: scores are
-//                read from tensor memory, the weights go back as bf16 over
-//                them, the accumulator is rescaled in place in the rare case that
-//                a row's maximum outgrows its reference;
+//   warps 0-3, 4-7  softmax of tile 0 and tile 1, one thread a row: the scores
+//                of a stage are read from tensor memory into registers, the
+//                weights go back as bf16 over them in two halves, and the
+//                accumulator is rescaled in place in the rare case that the row's
+//                maximum outgrows its reference;
 //   warps 8-11   query loads and epilogue;
 //   warps 12, 13 TMA loads of K and V, one block of 16 tokens a box;
-//   warps 14, 15 MMA issue, one thread each: S = Q K^T (operands in shared
-//                memory) and O += P V (P from tensor memory).
+//   warps 14, 15 MMA issue: S = Q K^T (operands in shared memory), and
+//                O += P V (P from tensor memory).
+// Tensor memory holds one score buffer, two weight buffers and two
+// accumulators.  The tiles take turns with the scores: a softmax warp copies its
+// row of 128 scores to registers and gives the buffer up before it computes
+// anything, so that the other tile's Q K^T, and this tile's next, never wait for an
+// exponential or a P V, and scores are there when a tile has finished a stage.
+// (With a score buffer per tile and the weights written over the scores, a tile's next
+// Q K^T had to wait for its P V: 5300 cycles a stage of 256 x 128 instead of TODO.)
 // Every wait is bounded (fca_device.cuh); a role that gives up sets the CTA's
 // abort flag, the others leave at their next wait, copies and MMAs in flight
 // are waited for, and tensor memory is freed.
@@ -45,16 +53,14 @@ constexpr int kStage = kChunkStage;
 constexpr int kBlkPerStage = kStage / kBlockSize;
 constexpr int kThreads = 512;
 constexpr int kEpiWarp0 = 8;
-constexpr int kKWarp = 12, kVWarp = 13, kQKWarp = 14;   // (15: P V)
+constexpr int kKWarp = 12, kVWarp = 13, kQKWarp = 14;
 // Registers a thread: the four warpgroups' shares add up to the launch's 128 each.
 constexpr int kRegsSoftmax = 184, kRegsEpilogue = 88, kRegsOthers = 56;
 static_assert(2 * kRegsSoftmax + kRegsEpilogue + kRegsOthers == 4 * 128, "register shares");
-// A row's exponentials use a reference that trails its running maximum: it is
-// moved (and the accumulator rescaled, a stage later) once the maximum is 2^8
-// above it, and at once, with the stage computed again, at 2^64.  Weights up to
-// 2^64 are exact powers away from their true size, well inside bf16 and fp32.
+// A row's exponentials are taken against a reference that follows its running
+// maximum only when that is 2^8 above it: the accumulator is rescaled in few stages, and
+// weights up to 2^8 are as exact in bf16 and fp32 as those up to 1.
 constexpr float kRescaleLog2 = 8.f;
-constexpr float kRedoLog2 = 64.f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 struct ChunkArgs {
@@ -71,7 +77,6 @@ struct ChunkArgs {
     float* lse;
     float* part_o;
     float* part_w;
-    float* part_lse;
     int32_t part_rows, max_blocks, num_blocks, Hq, Hkv, G;
     float scale_log2;
     int32_t* err;
@@ -82,17 +87,18 @@ struct Layout {
     static constexpr int kHalves = D / 64;               // 128-byte swizzle atoms a row
     static constexpr int kTileQ = 128 * D * 2;
     static constexpr int kKV = kStage * D * 2;           // one K or V stage
-    static constexpr int kSlots = D == 128 ? 2 : 4;      // of K, and of V
+    static constexpr int kKSlots = D == 128 ? 3 : 5;
+    static constexpr int kVSlots = D == 128 ? 2 : 5;
     static constexpr int kOffQ = 0;                      // two tiles
     static constexpr int kOffK = kOffQ + 2 * kTileQ;
-    static constexpr int kOffV = kOffK + kSlots * kKV;
-    static constexpr int kOffML = kOffV + kSlots * kKV;  // [2][3][128] f32: row reference, sum, sum of rounded
-    static constexpr int kOffBar = kOffML + 2 * 3 * 128 * 4;
-    static constexpr int kNumBars = 4 * kSlots + 2 + 7 * 2 + 1;
+    static constexpr int kOffV = kOffK + kKSlots * kKV;
+    static constexpr int kOffML = kOffV + kVSlots * kKV; // [2][2][128] f32: a row's reference and sum
+    static constexpr int kOffBar = kOffML + 2 * 2 * 128 * 4;
+    static constexpr int kNumBars = 2 * (kKSlots + kVSlots) + 10 * 2 + 2;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-    static constexpr int kBytes = kOffMisc + 32;
-    static constexpr int kAlloc = kBytes + 1024;         // the operands want 1024-byte alignment
-    static constexpr uint32_t kColS = 0;                 // tile t's scores: 128 fp32 columns at 128 t
+    static constexpr int kAlloc = kOffMisc + 32;
+    static constexpr uint32_t kColS = 0;                 // scores: 128 fp32 columns
+    static constexpr uint32_t kColP = 128;               // tile t's weights: 64 columns of bf16 pairs at 128 + 64 t
     static constexpr uint32_t kColO = 256;               // tile t's accumulator: D columns at 256 + D t
     static constexpr uint32_t kTmemCols = 512;
     static_assert(kColO + 2 * D <= kTmemCols, "tensor memory budget");
@@ -149,65 +155,55 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32
 }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// Maximum of a row's scores (raw q.k) in columns below nv.
-template <bool MASK>
-__device__ __forceinline__ float row_max(uint32_t s_addr, int nv) {
-    float mx = -INFINITY;
+// Waits for this thread's tensor-memory loads; the registers are named so that
+// no use of them can be moved before the wait.
+__device__ __forceinline__ void wait_ld(uint32_t (&x)[32], uint32_t (&y)[32]) {
+    dev::tc_wait_ld();
 #pragma unroll
-    for (int c = 0; c < kStage; c += 32) {
-        uint32_t r[32];
-        dev::tmem_ld32(s_addr + c, r);
-        dev::tc_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            const float x = (!MASK || c + i < nv) ? __uint_as_float(r[i]) : -INFINITY;
-            const float y = (!MASK || c + i + 1 < nv) ? __uint_as_float(r[i + 1]) : -INFINITY;
-            mx = dev::max3(mx, x, y);
-        }
+    for (int i = 0; i < 32; i += 4) {
+        asm volatile("" : "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]));
+        asm volatile("" : "+r"(y[i]), "+r"(y[i + 1]), "+r"(y[i + 2]), "+r"(y[i + 3]));
     }
-    return mx;
 }
 
-// Weights of a row's stage against the reference m (log2 domain): bf16 pairs
-// in pw, their sum in sr and, for the lse, the sum before rounding in se.
-// Returns the maximum of the raw scores.
-template <bool MASK, bool LSE>
-__device__ __forceinline__ float row_weights(uint32_t s_addr, int nv, float scale_log2, float m, uint32_t (&pw)[kStage / 2],
-                                             float& se, float& sr) {
-    float2 e = make_float2(0.f, 0.f), q = make_float2(0.f, 0.f);
-    float mx = -INFINITY;
-    const float2 sc = make_float2(scale_log2, scale_log2), nm = make_float2(-m, -m);
+__device__ __forceinline__ float as_f(uint32_t x) { return __uint_as_float(x); }
+
+// Columns c .. c + 31 of a row from nv on to -inf.
+__device__ __forceinline__ void mask32(uint32_t (&x)[32], int c, int nv) {
 #pragma unroll
-    for (int c = 0; c < kStage; c += 64) {
-        uint32_t r0[32], r1[32];
-        dev::tmem_ld32(s_addr + c, r0);
-        dev::tmem_ld32(s_addr + c + 32, r1);
-        dev::tc_wait_ld();
+    for (int i = 0; i < 32; ++i) x[i] = c + i < nv ? x[i] : 0xff800000u;
+}
+
+__device__ __forceinline__ void max32(const uint32_t (&x)[32], float& a, float& b) {
 #pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-            float x = __uint_as_float(i < 32 ? r0[i & 31] : r1[i & 31]);
-            float y = __uint_as_float(i < 32 ? r0[(i + 1) & 31] : r1[(i + 1) & 31]);
-            if (MASK) {
-                x = c + i < nv ? x : -INFINITY;
-                y = c + i + 1 < nv ? y : -INFINITY;
-            }
-            mx = dev::max3(mx, x, y);
-            const float2 z = dev::fma2(make_float2(x, y), sc, nm);
-            const float2 p = make_float2(dev::ex2(z.x), dev::ex2(z.y));
-            const uint32_t w = dev::pack_bf16x2(p.x, p.y);
-            pw[(c + i) / 2] = w;
-            if (LSE) e = dev::add2(e, p);
-            q = dev::add2(q, make_float2(dev::bf16_lo(w), dev::bf16_hi(w)));
-        }
+    for (int i = 0; i < 32; i += 4) {
+        a = dev::max3(a, as_f(x[i]), as_f(x[i + 1]));
+        b = dev::max3(b, as_f(x[i + 2]), as_f(x[i + 3]));
     }
-    se = e.x + e.y;
-    sr = q.x + q.y;
-    return mx;
+}
+
+// Weights of 32 scores against the reference (nm = -m): 16 bf16 pairs, and their sum
+// before rounding.
+__device__ __forceinline__ void weights32(const uint32_t (&x)[32], float2 sc, float2 nm, uint32_t* p, float2& sum) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        const float2 z = dev::fma2(make_float2(as_f(x[i]), as_f(x[i + 1])), sc, nm);
+        const float2 e = make_float2(dev::ex2(z.x), dev::ex2(z.y));
+        p[i / 2] = dev::pack_bf16x2(e.x, e.y);
+        sum = dev::add2(sum, e);
+    }
 }
 
 // One row by one warp with plain arithmetic, lane i holding D / 32 of the
@@ -243,31 +239,34 @@ __device__ __noinline__ void exact_row(const ChunkArgs& a, int32_t req, int32_t 
     }
 }
 
-template <int D, bool LSE>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     k_chunk(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
             const __grid_constant__ CUtensorMap tmV) {
     using L = Layout<D>;
-    constexpr int NS = L::kSlots;
     const int32_t first = a.begin[blockIdx.x], last = a.end[blockIdx.x];
     if (first >= last) return;
 
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
-    uint64_t* k_full = bars;                // [NS] a K slot holds its stage
-    uint64_t* k_empty = k_full + NS;        // [NS] the products reading it have completed
-    uint64_t* v_full = k_empty + NS;        // [NS]
-    uint64_t* v_empty = v_full + NS;        // [NS]
-    uint64_t* q_full = v_empty + NS;        // the item's queries are written
-    uint64_t* q_free = q_full + 1;          // the item's last Q K^T has completed
-    uint64_t* s_full = q_free + 1;          // [2] a stage's scores are in the tile's columns
-    uint64_t* p_full = s_full + 2;          // [2] its weights are written over them
-    uint64_t* pv_done = p_full + 2;         // [2] the P V reading them has completed
-    uint64_t* o_full = pv_done + 2;         // [2] an item's last P V of the tile has completed
-    uint64_t* o_free = o_full + 2;          // [2] the epilogue has read the accumulator
-    uint64_t* ml_full = o_free + 2;         // [2] the tile's row state is written
-    uint64_t* ml_free = ml_full + 2;        // [2] ... and read
+    extern __shared__ __align__(1024) uint8_t smem[];    // the swizzled operands want 1024-byte alignment
+    if (dev::smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0) atomicOr(a.err, kErrBadItem);
+        return;
+    }
+    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L::kOffBar);   // [slots] a K slot holds its stage
+    uint64_t* k_empty = k_full + L::kKSlots;   // [slots] the products of both tiles reading it have completed
+    uint64_t* v_full = k_empty + L::kKSlots;   // [slots]
+    uint64_t* v_empty = v_full + L::kVSlots;   // [slots]
+    uint64_t* q_full = v_empty + L::kVSlots;   // [2] a query tile is written
+    uint64_t* q_free = q_full + 2;             // [2] the last products reading it have completed
+    uint64_t* s_full = q_free + 2;             // [2] a stage's scores of the tile are there
+    uint64_t* s_free = s_full + 2;             // ... and copied
+    uint64_t* p_half = s_free + 1;             // [2] the first half of the tile's weights is written
+    uint64_t* p_full = p_half + 2;             // [2] ... all of them
+    uint64_t* pv_done = p_full + 2;            // [2] the P V reading them has completed
+    uint64_t* o_full = pv_done + 2;            // [2] an item's last P V of the tile has completed
+    uint64_t* o_free = o_full + 2;             // [2] the epilogue has read the accumulator
+    uint64_t* ml_full = o_free + 2;            // [2] the tile's row state is written
+    uint64_t* ml_free = ml_full + 2;           // [2] ... and read
     uint64_t* mma_done = ml_free + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 16);
@@ -275,16 +274,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < NS; ++s) {
+        for (int s = 0; s < L::kKSlots; ++s) {
             dev::mbar_init(&k_full[s], 1);
             dev::mbar_init(&k_empty[s], 1);
+        }
+        for (int s = 0; s < L::kVSlots; ++s) {
             dev::mbar_init(&v_full[s], 1);
             dev::mbar_init(&v_empty[s], 1);
         }
-        dev::mbar_init(q_full, 128);
-        dev::mbar_init(q_free, 1);
         for (int t = 0; t < 2; ++t) {
+            dev::mbar_init(&q_full[t], 128);
+            dev::mbar_init(&q_free[t], 1);
             dev::mbar_init(&s_full[t], 1);
+            dev::mbar_init(&p_half[t], 128);
             dev::mbar_init(&p_full[t], 128);
             dev::mbar_init(&pv_done[t], 1);
             dev::mbar_init(&o_full[t], 1);
@@ -292,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             dev::mbar_init(&ml_full[t], 128);
             dev::mbar_init(&ml_free[t], 128);
         }
+        dev::mbar_init(s_free, 128);
         dev::mbar_init(mma_done, 2);
         *abort_flag = 0;
         dev::fence_mbarrier_init();
@@ -307,12 +310,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < kEpiWarp0) {
         // ------------------------------------------------ softmax
-        // m_ref is the reference of new exponentials; the accumulator and the
-        // sums are relative to m_used, which follows a stage later.
         regs_inc<kRegsSoftmax>();
         const int t = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        const uint32_t s_addr = tmem + lane_base + L::kColS + t * 128, o_addr = tmem + lane_base + L::kColO + t * D;
+        const uint32_t s_addr = tmem + lane_base + L::kColS, p_addr = tmem + lane_base + L::kColP + t * 64,
+                       o_addr = tmem + lane_base + L::kColO + t * D;
         bool ok = true;
         uint32_t g = 0;                 // stages of this tile so far
         uint32_t gv = 0;                // stages of the CTA before the item
@@ -329,86 +331,105 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r_item = w.dual ? row : t * 128 + row;             // stacked row within the item
             const bool live = (w.dual ? quarter * 32 : t * 128 + quarter * 32) < w.it.nrows;
             const int32_t lim = row_limit(w.it, min(r_item, w.it.nrows - 1), a.G) - w.it.tok0;   // tokens of the item it sees
-            float m_ref = -INFINITY, m_used = -INFINITY, l_exact = 0.f, l_round = 0.f;
+            float m = -INFINITY, l = 0.f;       // reference (log2 domain) and sum of the weights
+            // the tile whose P V comes first clears the last stage's tail
+            const bool clears = w.it.tok1 % kBlockSize != 0 && (w.dual || t == 0 || w.ns0 < w.ns);
             for (int32_t x = 0; x < ns; ++x, ++g) {
                 const int32_t j = w.dual ? 2 * x + t : x;
                 bool got = dev::mbar_wait(&s_full[t], g & 1, abort_flag, a.err);
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 dev::tc_fence_after();
-                // (the scores were issued after the tile's last P V completed: the accumulator is up to date)
-                if (live) {
-                    const int nv = min(kStage, max(0, lim - j * kStage));
-                    const bool mask = __any_sync(0xffffffffu, nv < kStage);
-                    float o_scale = 1.f;
-                    if (m_used != m_ref) {                       // a move owed by the previous stage
-                        o_scale = dev::ex2(m_used - m_ref);
-                        l_exact *= o_scale;
-                        l_round *= o_scale;
-                        m_used = m_ref;
-                    }
-                    if (__any_sync(0xffffffffu, m_ref == -INFINITY)) {   // rows that have seen nothing yet
-                        const float mx = mask ? row_max<true>(s_addr, nv) : row_max<false>(s_addr, nv);
-                        if (m_ref == -INFINITY) m_ref = m_used = mx * a.scale_log2;
-                    }
-                    uint32_t pw[kStage / 2];
-                    float se = 0.f, sr = 0.f;
-#pragma unroll 1
-                    for (int attempt = 0;; ++attempt) {
-                        const float m0 = m_ref == -INFINITY ? 0.f : m_ref;      // nothing seen: every weight is 2^-inf
-                        const float mx = (mask ? row_weights<true, LSE>(s_addr, nv, a.scale_log2, m0, pw, se, sr)
-                                               : row_weights<false, LSE>(s_addr, nv, a.scale_log2, m0, pw, se, sr)) *
-                                         a.scale_log2;           // the scale is positive
-                        const bool redo = attempt == 0 && mx > m_ref + kRedoLog2;
-                        if (__any_sync(0xffffffffu, redo)) {
-                            if (redo) {
-                                const float f = dev::ex2(m_ref - mx);
-                                l_exact *= f;
-                                l_round *= f;
-                                o_scale *= f;
-                                m_ref = m_used = mx;
-                            }
-                            continue;
+                // Before the stage's first weights: the P V of the tile's stage before has
+                // read the last ones.  And the last block's slots behind the range were
+                // loaded too and may hold anything, NaN included: their weights are 0, but
+                // 0 x NaN is not, so V's rows there are cleared.
+                auto ready = [&](bool waited) -> bool {
+                    bool up = waited || g == 0 || dev::mbar_wait(&pv_done[t], (g - 1) & 1, abort_flag, a.err);
+                    if (clears && j == w.ns - 1) {
+                        const uint32_t s = (gv + j) % L::kVSlots;
+                        up = up && dev::mbar_wait(&v_full[s], ((gv + j) / L::kVSlots) & 1, abort_flag, a.err);
+                        const int r0 = w.it.tok1 - w.it.tok0 - j * kStage, r1 = (r0 + kBlockSize - 1) / kBlockSize * kBlockSize;
+                        uint8_t* vs = smem + L::kOffV + s * L::kKV;
+                        for (int e = row; up && e < (r1 - r0) * 8 * L::kHalves; e += 128) {
+                            const int rr = r0 + e / (8 * L::kHalves), c = e % (8 * L::kHalves);
+                            *reinterpret_cast<uint4*>(vs + sw128_off(rr, c >> 3, c & 7)) = make_uint4(0, 0, 0, 0);
                         }
-                        if (mx > m_ref + kRescaleLog2) m_ref = mx;      // moved at the next stage
-                        break;
+                        dev::fence_proxy_async_smem();
                     }
-                    l_exact += se;
-                    l_round += sr;
-                    if (__any_sync(0xffffffffu, o_scale != 1.f)) {
-#pragma unroll 1
-                        for (int c = 0; c < D / 16; ++c) {
-                            uint32_t ov[16];
-                            dev::tmem_ld16(o_addr + c * 16, ov);
-                            dev::tc_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * o_scale);
-                            dev::tmem_st16(o_addr + c * 16, ov);
-                        }
-                    }
-                    uint32_t p0[32], p1[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        p0[e] = pw[e];
-                        p1[e] = pw[32 + e];
-                    }
-                    dev::tmem_st32(s_addr, p0);
-                    dev::tmem_st32(s_addr + 32, p1);
+                    dev::tc_fence_after();
+                    return __all_sync(0xffffffffu, up);
+                };
+                if (!live) {
+                    dev::mbar_arrive(s_free);
+                    if (!ready(false)) { ok = false; break; }
+                    dev::mbar_arrive(&p_half[t]);
+                    dev::mbar_arrive(&p_full[t]);
+                    continue;
                 }
-                if (j == w.ns - 1 && (w.dual || t == 1) && w.it.tok1 % kBlockSize) {
-                    // The last block's slots behind the range were loaded too and may
-                    // hold anything, NaN included: their weights are 0, but 0 x NaN is
-                    // not, so V's rows there are cleared.
-                    const uint32_t s = (gv + j) % NS;
-                    got = dev::mbar_wait(&v_full[s], ((gv + j) / NS) & 1, abort_flag, a.err);
+                uint32_t s0[32], s1[32], s2[32], s3[32];
+                dev::tmem_ld32(s_addr, s0);
+                dev::tmem_ld32(s_addr + 32, s1);
+                dev::tmem_ld32(s_addr + 64, s2);
+                dev::tmem_ld32(s_addr + 96, s3);
+                wait_ld(s0, s1);
+                wait_ld(s2, s3);
+                dev::tc_fence_before();
+                dev::mbar_arrive(s_free);
+                const int nv = lim - j * kStage;                 // columns that the row sees
+                if (__any_sync(0xffffffffu, nv < kStage)) {
+                    mask32(s0, 0, nv);
+                    mask32(s1, 32, nv);
+                    mask32(s2, 64, nv);
+                    mask32(s3, 96, nv);
+                }
+                float mx = -INFINITY, my = -INFINITY, mz = -INFINITY, mw = -INFINITY;
+                max32(s0, mx, my);
+                max32(s1, mz, mw);
+                max32(s2, mx, my);
+                max32(s3, mz, mw);
+                mx = fmaxf(dev::max3(mx, my, mz), mw) * a.scale_log2;        // the scale is positive
+                float f = 1.f;
+                if (mx > m + kRescaleLog2) {
+                    f = dev::ex2(m - mx);
+                    l *= f;
+                    m = mx;
+                }
+                bool waited = false;
+                // (an item's first P V overwrites the accumulator)
+                if (x > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+                    got = dev::mbar_wait(&pv_done[t], (g - 1) & 1, abort_flag, a.err);
                     if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-                    const int r0 = w.it.tok1 - w.it.tok0 - j * kStage, r1 = (r0 + kBlockSize - 1) / kBlockSize * kBlockSize;
-                    uint8_t* vs = smem + L::kOffV + s * L::kKV;
-                    for (int e = row; e < (r1 - r0) * 8 * L::kHalves; e += 128) {
-                        const int rr = r0 + e / (8 * L::kHalves), c = e % (8 * L::kHalves);
-                        *reinterpret_cast<uint4*>(vs + sw128_off(rr, c >> 3, c & 7)) = make_uint4(0, 0, 0, 0);
+                    waited = true;
+                    dev::tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t ov[16];
+                        dev::tmem_ld16(o_addr + c * 16, ov);
+                        dev::tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            asm volatile("" : "+r"(ov[e]));
+                            ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f);
+                        }
+                        dev::tmem_st16(o_addr + c * 16, ov);
                     }
-                    dev::fence_proxy_async_smem();
                 }
+                const float m0 = m == -INFINITY ? 0.f : m;       // nothing seen yet: every weight is 2^-inf
+                const float2 sc = make_float2(a.scale_log2, a.scale_log2), nm = make_float2(-m0, -m0);
+                float2 sum = make_float2(0.f, 0.f), sum2 = make_float2(0.f, 0.f);
+                uint32_t p[32];
+                weights32(s0, sc, nm, p, sum);
+                weights32(s1, sc, nm, p + 16, sum2);
+                if (!ready(waited)) { ok = false; break; }
+                dev::tmem_st32(p_addr, p);
+                dev::tc_wait_st();
+                dev::tc_fence_before();
+                dev::mbar_arrive(&p_half[t]);
+                weights32(s2, sc, nm, p, sum);
+                weights32(s3, sc, nm, p + 16, sum2);
+                dev::tmem_st32(p_addr + 32, p);
+                sum = dev::add2(sum, sum2);
+                l += sum.x + sum.y;
                 dev::tc_wait_st();
                 dev::tc_fence_before();
                 dev::mbar_arrive(&p_full[t]);
@@ -420,9 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool got = dev::mbar_wait(&ml_free[t], (n_items - 1) & 1, abort_flag, a.err);
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
             }
-            ml[t * 384 + row] = m_used;
-            ml[t * 384 + 128 + row] = l_round;
-            if (LSE) ml[t * 384 + 256 + row] = l_exact;
+            ml[t * 256 + row] = m;
+            ml[t * 256 + 128 + row] = l;
             dev::mbar_arrive(&ml_full[t]);
             ++n_items;
         }
@@ -432,65 +452,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int quarter = warp & 3, tid = threadIdx.x - kEpiWarp0 * 32, row = quarter * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t q_smem = dev::smem_u32(smem + L::kOffQ);
+        // Query tile b of an item, once the products of the tile's last queries have completed.
+        uint32_t n_q[2] = {0, 0};
+        bool ok = true;
         auto load_q = [&](const Work& w) {
             constexpr int C = D / 8;            // 16-byte chunks a row
-            const int rows = w.dual ? 128 : 256;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                if (b ? w.dual : w.ns0 == 0) continue;
+                if (n_q[b]) {
+                    bool got = dev::mbar_wait(&q_free[b], (n_q[b] - 1) & 1, abort_flag, a.err);
+                    if (!__all_sync(0xffffffffu, got)) { ok = false; return; }
+                }
+                ++n_q[b];
 #pragma unroll 4
-            for (int e = tid; e < rows * C; e += 128) {
-                const int r = e / C, c = e % C;
-                const int32_t sr = w.it.row0 + min(r, w.it.nrows - 1);
-                const __nv_bfloat16* src =
-                    a.q + (int64_t)(w.it.q0 + sr / a.G) * a.q_stride + (w.it.head * a.G + sr % a.G) * D + c * 8;
-                cp_async16(q_smem + (r >> 7) * L::kTileQ + sw128_off(r & 127, c >> 3, c & 7), src, r < w.it.nrows ? 16u : 0u);
+                for (int e = tid; e < 128 * C; e += 128) {
+                    const int r = e / C, c = e % C, ri = b * 128 + r;
+                    const int32_t sr = w.it.row0 + min(ri, w.it.nrows - 1);
+                    const __nv_bfloat16* src =
+                        a.q + (int64_t)(w.it.q0 + sr / a.G) * a.q_stride + (w.it.head * a.G + sr % a.G) * D + c * 8;
+                    cp_async16(q_smem + b * L::kTileQ + sw128_off(r, c >> 3, c & 7), src, ri < w.it.nrows ? 16u : 0u);
+                }
+                cp_async_wait();
+                dev::fence_proxy_async_smem();
+                dev::mbar_arrive(&q_full[b]);
             }
-            cp_async_wait();
-            dev::fence_proxy_async_smem();
-            dev::mbar_arrive(q_full);
         };
-        // Rows of the item that this warp's threads hold in tile t: out and lse,
-        // or the piece's partial rows, from coefficients c0, c1 of the two accumulators.
-        bool ok = true;
-        uint32_t n_act = 0, n0 = 0, n1 = 0;     // items with stages; with stages for tile 0, tile 1
-        int32_t qi = first;
-        Work qw;
-        for (; qi < last; ++qi) {
-            qw = load_work(a, qi);
-            if (qw.ns) break;
-        }
-        if (qi < last) load_q(qw);
+        uint32_t n0 = 0, n1 = 0;                // items with stages for tile 0, tile 1
+        int32_t qi = first;                     // the item whose queries are loaded next
+        auto load_next = [&](int32_t from) {
+            for (qi = from; qi < last; ++qi) {
+                const Work qw = load_work(a, qi);
+                if (qw.ns) {
+                    load_q(qw);
+                    return;
+                }
+            }
+        };
+        load_next(first);
         for (int32_t i = first; ok && i < last; ++i) {
             const Work w = load_work(a, i);
-            if (w.ns) {
-                for (qi = i + 1; qi < last; ++qi) {
-                    qw = load_work(a, qi);
-                    if (qw.ns) break;
-                }
-                if (qi < last) {
-                    bool got = dev::mbar_wait(q_free, n_act & 1, abort_flag, a.err);
-                    if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-                    load_q(qw);
-                }
-                ++n_act;
-            }
+            if (w.ns) load_next(i + 1);
+            if (!ok) break;
+            // Rows that this warp's threads hold: out and lse, or the piece's partial rows.
             for (int t = 0; t < (w.dual ? 1 : 2); ++t) {
                 // the tiles whose accumulators make up these rows
                 const bool use0 = t == 0 && w.ns0 > 0, use1 = (t == 1 || w.dual) && w.ns1 > 0;
-                float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, e0 = 0.f, e1 = 0.f;
+                float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
                 bool got = true;
                 if (use0) {
                     got = dev::mbar_wait(&ml_full[0], n0 & 1, abort_flag, a.err);
                     m0 = ml[row];
                     l0 = ml[128 + row];
-                    if (LSE) e0 = ml[256 + row];
                     dev::mbar_arrive(&ml_free[0]);
                     got = got && dev::mbar_wait(&o_full[0], n0 & 1, abort_flag, a.err);
                     ++n0;
                 }
                 if (use1) {
                     got = got && dev::mbar_wait(&ml_full[1], n1 & 1, abort_flag, a.err);
-                    m1 = ml[384 + row];
-                    l1 = ml[384 + 128 + row];
-                    if (LSE) e1 = ml[384 + 256 + row];
+                    m1 = ml[256 + row];
+                    l1 = ml[256 + 128 + row];
                     dev::mbar_arrive(&ml_free[1]);
                     got = got && dev::mbar_wait(&o_full[1], n1 & 1, abort_flag, a.err);
                     ++n1;
@@ -547,14 +568,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (use0) dev::mbar_arrive(&o_free[0]);
                     if (use1) dev::mbar_arrive(&o_free[1]);
                 }
-                const float le = LSE ? M + log2f(e0 * f0 + e1 * f1) : 0.f;      // -inf for a row that saw nothing
+                const float lw = M + log2f(l);      // -inf for a row that saw nothing
                 if (mine) {
-                    if (!whole) {
-                        a.part_w[prow] = M + log2f(l);
-                        if (LSE) a.part_lse[prow] = le;
-                    } else if (LSE) {
-                        a.lse[orow] = le * kLn2;
-                    }
+                    if (!whole)
+                        a.part_w[prow] = lw;
+                    else if (a.lse)
+                        a.lse[orow] = lw * kLn2;
                 }
                 // A product of weight 0 with an inf or NaN that the row does not see
                 // (a later token's) is NaN: rows that are not finite are computed
@@ -580,14 +599,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else
                             a.part_o[r_part * D + col] = o[e] * scale;
                     }
-                    const float lw = m + log2f(ls);
                     if (lane == 0) {
-                        if (!whole) {
-                            a.part_w[r_part] = lw;
-                            if (LSE) a.part_lse[r_part] = lw;
-                        } else if (LSE) {
-                            a.lse[r_out] = lw * kLn2;
-                        }
+                        const float lr = m + log2f(ls);
+                        if (!whole)
+                            a.part_w[r_part] = lr;
+                        else if (a.lse)
+                            a.lse[r_out] = lr * kLn2;
                     }
                 }
             }
@@ -596,12 +613,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_dec<kRegsOthers>();
         if (warp == kKWarp || warp == kVWarp) {
             // -------------------------------------------- TMA loads
-            // Stage g of the CTA goes to slot g % NS of its ring.  Block ids are
+            // Stage g of the CTA goes to slot g % slots of its ring.  Block ids are
             // read 32 at a time (four stages), a batch ahead.
             const bool is_k = warp == kKWarp;
             const CUtensorMap* tm = is_k ? &tmK : &tmV;
             uint64_t* full = is_k ? k_full : v_full;
             uint64_t* empty = is_k ? k_empty : v_empty;
+            const uint32_t NS = is_k ? L::kKSlots : L::kVSlots;
             uint8_t* const ring = smem + (is_k ? L::kOffK : L::kOffV);
             if (lane == 0) dev::tma_prefetch_desc(tm);
             constexpr int kStagesPerBatch = 32 / kBlkPerStage;
@@ -654,92 +672,113 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (uint32_t j = g; j > 0 && j + NS > g; --j)
                     dev::mbar_wait(&full[(j - 1) % NS], ((j - 1) / NS) & 1, &never, a.err);
             }
-        } else if (lane == 0) {
+        } else {
             // -------------------------------------------- MMA issue
+            // The whole warp runs the loop, so that descriptors are computed in uniform
+            // registers; one elected thread issues.
             bool ok = true;
-            uint32_t g = 0;                 // stages of the CTA so far
-            uint32_t c[2] = {0, 0};         // ... of each tile
-            uint32_t n_act = 0, n_tile[2] = {0, 0};
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                if (ok) ok = __all_sync(0xffffffffu, dev::mbar_wait(bar, parity, abort_flag, a.err));
+                return ok;
+            };
+            uint32_t g = 0;                     // stages of the CTA before the item
             Work nxt = load_work(a, first);
-            for (int32_t i = first; ok && i < last; ++i) {
-                const Work w = nxt;
-                if (i + 1 < last) nxt = load_work(a, i + 1);
-                if (w.ns == 0) continue;
-                if (warp == kQKWarp) {
-                    constexpr uint32_t idesc = dev::idesc_bf16_f32(128, kStage, false, false);
-                    ok = dev::mbar_wait(q_full, n_act & 1, abort_flag, a.err);
-                    ++n_act;
-                    for (int32_t j = 0; ok && j < w.ns; ++j, ++g) {
-                        const uint32_t s = g % NS;
-                        if (!dev::mbar_wait(&k_full[s], (g / NS) & 1, abort_flag, a.err)) { ok = false; break; }
-                        const uint32_t k_base = dev::smem_u32(smem + L::kOffK) + s * L::kKV;
+            if (warp == kQKWarp) {
+                constexpr uint32_t idesc = dev::idesc_bf16_f32(128, kStage, false, false);
+                const uint64_t q_desc = dev::smem_desc_sw128(dev::smem_u32(smem + L::kOffQ), 16, 1024);
+                const uint64_t k_desc = dev::smem_desc_sw128(dev::smem_u32(smem + L::kOffK), 16, 1024);
+                uint32_t n = 0;                 // score tiles so far
+                uint32_t loads0 = 0, loads1 = 0;   // query loads so far, by buffer
+                for (int32_t i = first; ok && i < last; ++i) {
+                    const Work w = nxt;
+                    if (i + 1 < last) nxt = load_work(a, i + 1);
+                    if (w.ns == 0) continue;
+                    if (w.dual || w.ns0) ++loads0;
+                    if (!w.dual) ++loads1;
+                    for (int32_t j = 0; ok && j < w.ns; ++j) {
+                        const uint32_t G = g + j, s = G % L::kKSlots;
+                        wait(&k_full[s], (G / L::kKSlots) & 1);
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             if (w.dual ? (j & 1) != t : (t == 0 && j >= w.ns0)) continue;
-                            // the weights that lie over the tile's scores have been used
-                            if (c[t] >= 1 && !dev::mbar_wait(&pv_done[t], (c[t] - 1) & 1, abort_flag, a.err)) {
-                                ok = false;
-                                break;
-                            }
+                            const int b = w.dual ? 0 : t;
+                            if (j == 0) wait(&q_full[b], ((b ? loads1 : loads0) - 1) & 1);
+                            if (n) wait(s_free, (n - 1) & 1);
+                            if (!ok) break;
                             dev::tc_fence_after();
-                            const uint32_t q_base = dev::smem_u32(smem + L::kOffQ) + (w.dual ? 0 : t) * L::kTileQ;
+                            const uint64_t ad0 = q_desc + ((uint32_t)(b * L::kTileQ) >> 4), bd0 = k_desc + ((s * L::kKV) >> 4);
+                            if (elect_one()) {
 #pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {
-                                const uint64_t ad = dev::smem_desc_sw128(q_base + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024);
-                                const uint64_t bd = dev::smem_desc_sw128(k_base + (k >> 2) * (kStage * 128) + (k & 3) * 32, 16, 1024);
-                                dev::tc_mma_ss(tmem + L::kColS + t * 128, ad, bd, idesc, k > 0 ? 1u : 0u);
+                                for (int k = 0; k < D / 16; ++k) {
+                                    const uint32_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+                                    dev::tc_mma_ss(tmem + L::kColS, ad0 + off, bd0 + off, idesc, k > 0 ? 1u : 0u);
+                                }
+                                dev::tc_commit(&s_full[t]);
+                                const int32_t ns_t = w.dual ? w.ns : (t ? w.ns1 : w.ns0);
+                                if (j + 1 == ns_t) dev::tc_commit(&q_free[b]);
                             }
-                            dev::tc_commit(&s_full[t]);
-                            ++c[t];
+                            __syncwarp();
+                            ++n;
                         }
                         if (!ok) break;
-                        dev::tc_commit(&k_empty[s]);
-                        if (j + 1 == w.ns) dev::tc_commit(q_free);
+                        if (elect_one()) dev::tc_commit(&k_empty[s]);
+                        __syncwarp();
                     }
-                } else {
-                    constexpr uint32_t idesc = dev::idesc_bf16_f32(128, D, false, true);
-                    const bool tail = w.it.tok1 % kBlockSize != 0;
-                    for (int32_t j = 0; ok && j < w.ns; ++j, ++g) {
-                        const uint32_t s = g % NS;
-                        if (!dev::mbar_wait(&v_full[s], (g / NS) & 1, abort_flag, a.err)) { ok = false; break; }
-                        // the tile-1 warps clear the last stage's tail for both tiles
-                        if (tail && !w.dual && j + 1 == w.ns && !dev::mbar_wait(&p_full[1], c[1] & 1, abort_flag, a.err)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t v_base = dev::smem_u32(smem + L::kOffV) + s * L::kKV;
+                    g += w.ns;
+                }
+            } else {
+                constexpr uint32_t idesc = dev::idesc_bf16_f32(128, D, false, true);
+                const uint64_t v_desc = dev::smem_desc_sw128(dev::smem_u32(smem + L::kOffV), kStage * 128, 1024);
+                uint32_t c[2] = {0, 0};         // P V so far, by tile
+                uint32_t n_tile[2] = {0, 0};    // items finished, by tile
+                for (int32_t i = first; ok && i < last; ++i) {
+                    const Work w = nxt;
+                    if (i + 1 < last) nxt = load_work(a, i + 1);
+                    if (w.ns == 0) continue;
+                    for (int32_t j = 0; ok && j < w.ns; ++j) {
+                        const uint32_t G = g + j, s = G % L::kVSlots;
+                        wait(&v_full[s], (G / L::kVSlots) & 1);
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             if (w.dual ? (j & 1) != t : (t == 0 && j >= w.ns0)) continue;
                             const int32_t x = w.dual ? j >> 1 : j, ns_t = t ? w.ns1 : w.ns0;
                             // a new item's accumulator starts once the epilogue has read the last one's
-                            if (x == 0 && n_tile[t] >= 1 &&
-                                !dev::mbar_wait(&o_free[t], (n_tile[t] - 1) & 1, abort_flag, a.err)) {
-                                ok = false;
-                                break;
-                            }
-                            if (!dev::mbar_wait(&p_full[t], c[t] & 1, abort_flag, a.err)) { ok = false; break; }
+                            if (x == 0 && n_tile[t]) wait(&o_free[t], (n_tile[t] - 1) & 1);
+                            const uint64_t bd0 = v_desc + ((s * L::kKV) >> 4);
+                            const uint32_t d = tmem + L::kColO + t * D, p = tmem + L::kColP + t * 64;
+                            wait(&p_half[t], c[t] & 1);
+                            if (!ok) break;
                             dev::tc_fence_after();
+                            if (elect_one()) {
 #pragma unroll
-                            for (int k = 0; k < kStage / 16; ++k) {
-                                const uint64_t bd = dev::smem_desc_sw128(v_base + k * (16 * 128), kStage * 128, 1024);
-                                dev::tc_mma_ts(tmem + L::kColO + t * D, tmem + L::kColS + t * 128 + k * 8, bd, idesc,
-                                               (x == 0 && k == 0) ? 0u : 1u);
+                                for (int k = 0; k < kStage / 32; ++k)
+                                    dev::tc_mma_ts(d, p + k * 8, bd0 + k * (16 * 128 / 16), idesc, (x == 0 && k == 0) ? 0u : 1u);
                             }
-                            dev::tc_commit(&pv_done[t]);
-                            if (x + 1 == ns_t) {
-                                dev::tc_commit(&o_full[t]);
-                                ++n_tile[t];
+                            __syncwarp();
+                            wait(&p_full[t], c[t] & 1);
+                            if (!ok) break;
+                            dev::tc_fence_after();
+                            if (elect_one()) {
+#pragma unroll
+                                for (int k = kStage / 32; k < kStage / 16; ++k)
+                                    dev::tc_mma_ts(d, p + k * 8, bd0 + k * (16 * 128 / 16), idesc, 1u);
+                                dev::tc_commit(&pv_done[t]);
+                                if (x + 1 == ns_t) dev::tc_commit(&o_full[t]);
                             }
+                            __syncwarp();
+                            if (x + 1 == ns_t) ++n_tile[t];
                             ++c[t];
                         }
                         if (!ok) break;
-                        dev::tc_commit(&v_empty[s]);
+                        if (elect_one()) dev::tc_commit(&v_empty[s]);
+                        __syncwarp();
                     }
+                    g += w.ns;
                 }
             }
-            // every MMA of this thread has retired before tensor memory is freed
-            dev::tc_commit(mma_done);
+            // every MMA of this warp has retired before tensor memory is freed
+            if (elect_one()) dev::tc_commit(mma_done);
+            __syncwarp();
             volatile int never = 0;
             dev::mbar_wait(mma_done, 0, &never, a.err);
         }
@@ -765,26 +804,19 @@ __global__ void __launch_bounds__(kMergeThreads) k_chunk_merge(ChunkArgs a, cons
     for (int32_t row = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); row < cut.nrows;
          row += kMergeSplit * (kMergeThreads / 32)) {
         auto at = [&](int p) { return (int64_t)(2 * (cut.cta0 + p) + (p == 0 ? 1 : 0)) * a.part_rows + row; };
-        float M = -INFINITY, Ml = -INFINITY;
-        for (int p = lane; p < pieces; p += 32) {
-            M = fmaxf(M, a.part_w[at(p)]);
-            if (a.lse) Ml = fmaxf(Ml, a.part_lse[at(p)]);
-        }
+        float M = -INFINITY;
+        for (int p = lane; p < pieces; p += 32) M = fmaxf(M, a.part_w[at(p)]);
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) {
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-            Ml = fmaxf(Ml, __shfl_xor_sync(0xffffffffu, Ml, x));
-        }
+        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
         if (M == -INFINITY) M = 0.f;
-        if (Ml == -INFINITY) Ml = 0.f;
-        float o[E], sum = 0.f, sl = 0.f;
+        float o[E], sum = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = 0.f;
         for (int base = 0; base < pieces; base += 32) {
             const int p = base + lane;
             const float f = p < pieces ? dev::ex2(a.part_w[at(p)] - M) : 0.f;
-            if (a.lse && p < pieces) sl += dev::ex2(a.part_lse[at(p)] - Ml);
             const int n = min(32, pieces - base);
+#pragma unroll 4
             for (int y = 0; y < n; ++y) {
                 const float fy = __shfl_sync(0xffffffffu, f, y);
                 const float* src = a.part_o + at(base + y) * D + lane * E;
@@ -802,32 +834,30 @@ __global__ void __launch_bounds__(kMergeThreads) k_chunk_merge(ChunkArgs a, cons
                 }
             }
         }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) sl += __shfl_xor_sync(0xffffffffu, sl, x);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int32_t sr = cut.row0 + row;
         const int64_t orow = (int64_t)(cut.q0 + sr / a.G) * a.Hq + cut.head * a.G + sr % a.G;
         uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + lane * E);
 #pragma unroll
         for (int e = 0; e < E; e += 2) dst[e / 2] = dev::pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-        if (a.lse && lane == 0) a.lse[orow] = (Ml + log2f(sl)) * kLn2;
+        if (a.lse && lane == 0) a.lse[orow] = (M + log2f(sum)) * kLn2;
     }
 }
 
-template <int D, bool LSE>
+template <int D>
 cudaError_t launch_chunk(const ChunkArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t stream) {
     using L = Layout<D>;
     // setmaxnreg hands out what the block was launched with: it has to have been 128 a thread
     static const cudaError_t ready = [] {
         cudaFuncAttributes at{};
-        cudaError_t e = cudaFuncGetAttributes(&at, k_chunk<D, LSE>);
+        cudaError_t e = cudaFuncGetAttributes(&at, k_chunk<D>);
         if (e == cudaSuccess && at.numRegs != 128) e = cudaErrorInvalidConfiguration;
         return e;
     }();
     if (ready != cudaSuccess) return ready;
-    cudaError_t e = cudaFuncSetAttribute(k_chunk<D, LSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+    cudaError_t e = cudaFuncSetAttribute(k_chunk<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
-    k_chunk<D, LSE><<<ctas, kThreads, L::kAlloc, stream>>>(a, tk, tv);
+    k_chunk<D><<<ctas, kThreads, L::kAlloc, stream>>>(a, tk, tv);
     return cudaGetLastError();
 }
 
@@ -865,7 +895,6 @@ extern "C" fca_status fca_chunk_attention(const void* q, int64_t q_row_stride, c
     a.lse = lse;
     a.part_o = plan->part_o;
     a.part_w = plan->part_w;
-    a.part_lse = plan->part_lse;
     a.part_rows = plan->part_rows;
     a.max_blocks = plan->max_blocks;
     a.num_blocks = plan->num_blocks;
@@ -874,11 +903,7 @@ extern "C" fca_status fca_chunk_attention(const void* q, int64_t q_row_stride, c
     a.G = plan->G;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = plan->dev_status;
-    cudaError_t e;
-    if (plan->D == 128)
-        e = lse ? launch_chunk<128, true>(a, tk, tv, plan->ctas, s) : launch_chunk<128, false>(a, tk, tv, plan->ctas, s);
-    else
-        e = lse ? launch_chunk<64, true>(a, tk, tv, plan->ctas, s) : launch_chunk<64, false>(a, tk, tv, plan->ctas, s);
+    const cudaError_t e = plan->D == 128 ? launch_chunk<128>(a, tk, tv, plan->ctas, s) : launch_chunk<64>(a, tk, tv, plan->ctas, s);
     if (note_cuda(e) != cudaSuccess) return FCA_ERR_CUDA;
     if (plan->may_cut) {
         const dim3 grid(plan->ctas, kMergeSplit);

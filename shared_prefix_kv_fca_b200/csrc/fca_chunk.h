@@ -69,7 +69,6 @@ struct fca_chunk_plan_s {
     int32_t* dev_status = nullptr;
     float* part_o = nullptr;        // [2 ctas][part_rows][D] normalised partial rows
     float* part_w = nullptr;        // [2 ctas][part_rows] log2 of their weights
-    float* part_lse = nullptr;      // [2 ctas][part_rows] log2-domain log-sum-exp
 
     void* base = nullptr;           // the one allocation
 };

@@ -305,7 +305,6 @@ size_t place(fca_chunk_plan_s* P, uint8_t* base) {
     put(&P->cuts, C);
     put(&P->part_o, 2 * C * P->part_rows * P->D);
     put(&P->part_w, 2 * C * P->part_rows);
-    put(&P->part_lse, 2 * C * P->part_rows);
     return at;
 }
 
