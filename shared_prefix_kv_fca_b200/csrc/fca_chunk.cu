@@ -78,6 +78,8 @@ struct ChunkArgs {
     float* part_o;
     float* part_w;
     int32_t part_rows, max_blocks, num_blocks, Hq, Hkv, G;
+    uint32_t div_g;     // 65536 / G, rounded up: x / G = x div_g >> 16 for x < kChunkRows + 16
+    int32_t q_tma;      // queries by TMA: G divides a tile
     float scale_log2;
     int32_t* err;
 };
@@ -94,7 +96,7 @@ struct Layout {
     static constexpr int kOffV = kOffK + kKSlots * kKV;
     static constexpr int kOffML = kOffV + kVSlots * kKV; // [2][2][128] f32: a row's reference and sum
     static constexpr int kOffBar = kOffML + 2 * 2 * 128 * 4;
-    static constexpr int kNumBars = 2 * (kKSlots + kVSlots) + 10 * 2 + 2;
+    static constexpr int kNumBars = 2 * (kKSlots + kVSlots) + 9 * 2 + 2;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
     static constexpr int kAlloc = kOffMisc + 32;
     static constexpr uint32_t kColS = 0;                 // scores: 128 fp32 columns
@@ -113,8 +115,18 @@ struct Work {
     bool dual;          // one tile of rows, stages dealt out to both
 };
 
-__device__ __forceinline__ int32_t row_limit(const ChunkItem& it, int32_t row, int32_t G) {
-    return min(it.tok1, it.lim0 + (it.row0 + row) / G + 1);
+__device__ __forceinline__ int32_t over_g(const ChunkArgs& a, int32_t x) { return (int32_t)((uint32_t)x * a.div_g >> 16); }
+
+// Tokens below which stacked row `row` of the item sees.
+__device__ __forceinline__ int32_t row_limit(const ChunkArgs& a, const ChunkItem& it, int32_t row) {
+    return min(it.tok1, it.lim0 + over_g(a, it.rem + row) + 1);
+}
+
+// Row of q (and of out, in heads) that stacked row `row` is.
+__device__ __forceinline__ int32_t row_token(const ChunkArgs& a, const ChunkItem& it, int32_t row, int32_t& qhead) {
+    const int32_t x = it.rem + row, t = over_g(a, x);
+    qhead = it.head * a.G + x - t * a.G;
+    return it.q0 + t;
 }
 
 __device__ __forceinline__ Work load_work(const ChunkArgs& a, int32_t i) {
@@ -124,7 +136,7 @@ __device__ __forceinline__ Work load_work(const ChunkArgs& a, int32_t i) {
     w.it.req = x.x;
     w.it.head = x.y;
     w.it.q0 = x.z;
-    w.it.row0 = x.w;
+    w.it.rem = x.w;
     w.it.nrows = y.x;
     w.it.tok0 = y.y;
     w.it.tok1 = y.z;
@@ -138,7 +150,7 @@ __device__ __forceinline__ Work load_work(const ChunkArgs& a, int32_t i) {
         w.ns1 = w.ns / 2;
     } else {
         // tile 1 holds the item's last row and has all its stages
-        w.ns0 = (max(0, row_limit(w.it, 127, a.G) - w.it.tok0) + kStage - 1) / kStage;
+        w.ns0 = (max(0, row_limit(a, w.it, 127) - w.it.tok0) + kStage - 1) / kStage;
         w.ns1 = w.ns;
     }
     return w;
@@ -242,7 +254,7 @@ __device__ __noinline__ void exact_row(const ChunkArgs& a, int32_t req, int32_t 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     k_chunk(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
-            const __grid_constant__ CUtensorMap tmV) {
+            const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ) {
     using L = Layout<D>;
     const int32_t first = a.begin[blockIdx.x], last = a.end[blockIdx.x];
     if (first >= last) return;
@@ -260,8 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* q_free = q_full + 2;             // [2] the last products reading it have completed
     uint64_t* s_full = q_free + 2;             // [2] a stage's scores of the tile are there
     uint64_t* s_free = s_full + 2;             // ... and copied
-    uint64_t* p_half = s_free + 1;             // [2] the first half of the tile's weights is written
-    uint64_t* p_full = p_half + 2;             // [2] ... all of them
+    uint64_t* p_full = s_free + 1;             // [2] the tile's weights are written
     uint64_t* pv_done = p_full + 2;            // [2] the P V reading them has completed
     uint64_t* o_full = pv_done + 2;            // [2] an item's last P V of the tile has completed
     uint64_t* o_free = o_full + 2;             // [2] the epilogue has read the accumulator
@@ -283,10 +294,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             dev::mbar_init(&v_empty[s], 1);
         }
         for (int t = 0; t < 2; ++t) {
-            dev::mbar_init(&q_full[t], 128);
+            dev::mbar_init(&q_full[t], a.q_tma ? 1 : 128);
             dev::mbar_init(&q_free[t], 1);
             dev::mbar_init(&s_full[t], 1);
-            dev::mbar_init(&p_half[t], 128);
             dev::mbar_init(&p_full[t], 128);
             dev::mbar_init(&pv_done[t], 1);
             dev::mbar_init(&o_full[t], 1);
@@ -330,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int r_item = w.dual ? row : t * 128 + row;             // stacked row within the item
             const bool live = (w.dual ? quarter * 32 : t * 128 + quarter * 32) < w.it.nrows;
-            const int32_t lim = row_limit(w.it, min(r_item, w.it.nrows - 1), a.G) - w.it.tok0;   // tokens of the item it sees
+            const int32_t lim = row_limit(a, w.it, min(r_item, w.it.nrows - 1)) - w.it.tok0;   // tokens of the item it sees
             float m = -INFINITY, l = 0.f;       // reference (log2 domain) and sum of the weights
             // the tile whose P V comes first clears the last stage's tail
             const bool clears = w.it.tok1 % kBlockSize != 0 && (w.dual || t == 0 || w.ns0 < w.ns);
@@ -362,7 +372,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!live) {
                     dev::mbar_arrive(s_free);
                     if (!ready(false)) { ok = false; break; }
-                    dev::mbar_arrive(&p_half[t]);
                     dev::mbar_arrive(&p_full[t]);
                     continue;
                 }
@@ -422,9 +431,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 weights32(s1, sc, nm, p + 16, sum2);
                 if (!ready(waited)) { ok = false; break; }
                 dev::tmem_st32(p_addr, p);
-                dev::tc_wait_st();
-                dev::tc_fence_before();
-                dev::mbar_arrive(&p_half[t]);
                 weights32(s2, sc, nm, p, sum);
                 weights32(s3, sc, nm, p + 16, sum2);
                 dev::tmem_st32(p_addr + 32, p);
@@ -460,18 +466,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 if (b ? w.dual : w.ns0 == 0) continue;
-                if (n_q[b]) {
+                if (n_q[b] && (!a.q_tma || warp == kEpiWarp0)) {
                     bool got = dev::mbar_wait(&q_free[b], (n_q[b] - 1) & 1, abort_flag, a.err);
                     if (!__all_sync(0xffffffffu, got)) { ok = false; return; }
                 }
                 ++n_q[b];
+                if (a.q_tma) {
+                    // (a tile's rows behind the request's are other requests' queries: computed
+                    // like the others and left alone)
+                    if (tid == 0) {
+                        dev::mbar_arrive_expect_tx(&q_full[b], L::kTileQ);
+                        for (int hf = 0; hf < L::kHalves; ++hf)
+                            dev::tma_load_3d(smem + L::kOffQ + b * L::kTileQ + hf * (128 * 128), &tmQ, &q_full[b], hf * 64,
+                                             w.it.head * a.G, w.it.q0 + over_g(a, b * 128));
+                    }
+                    continue;
+                }
 #pragma unroll 4
                 for (int e = tid; e < 128 * C; e += 128) {
                     const int r = e / C, c = e % C, ri = b * 128 + r;
-                    const int32_t sr = w.it.row0 + min(ri, w.it.nrows - 1);
-                    const __nv_bfloat16* src =
-                        a.q + (int64_t)(w.it.q0 + sr / a.G) * a.q_stride + (w.it.head * a.G + sr % a.G) * D + c * 8;
-                    cp_async16(q_smem + b * L::kTileQ + sw128_off(r, c >> 3, c & 7), src, ri < w.it.nrows ? 16u : 0u);
+                    int32_t qhead;
+                    const int32_t tok = row_token(a, w.it, min(ri, w.it.nrows - 1), qhead);
+                    cp_async16(q_smem + b * L::kTileQ + sw128_off(r, c >> 3, c & 7),
+                               a.q + (int64_t)tok * a.q_stride + qhead * D + c * 8, ri < w.it.nrows ? 16u : 0u);
                 }
                 cp_async_wait();
                 dev::fence_proxy_async_smem();
@@ -524,41 +541,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float f0 = dev::ex2(m0 - Mf), f1 = dev::ex2(m1 - Mf);
                 const float l = l0 * f0 + l1 * f1, inv = l == 0.f ? 0.f : 1.f / l;
                 const float c0 = f0 * inv, c1 = f1 * inv;
-                const int32_t sr = w.it.row0 + r_item;
-                const int64_t orow = (int64_t)(w.it.q0 + sr / a.G) * a.Hq + w.it.head * a.G + sr % a.G;
+                int32_t qhead;
+                const int32_t tok = row_token(a, w.it, r_item, qhead);
+                const int64_t orow = (int64_t)tok * a.Hq + qhead;
                 const int64_t prow = (int64_t)w.it.slot * a.part_rows + r_item;
                 float* const po = a.part_o + prow * D;
                 __nv_bfloat16* const bo = a.out + orow * D;
                 const bool whole = w.it.slot < 0;
                 float finite = 0.f;             // NaN once an element is not finite
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                    float v[32];
-                    uint32_t x[32];
+                for (int c = 0; c < D; c += 16) {
+                    float v[16];
+                    uint32_t x[16];
                     if (use0) {
-                        dev::tmem_ld32(tmem + lane_base + L::kColO + c, x);
+                        dev::tmem_ld16(tmem + lane_base + L::kColO + c, x);
                         dev::tc_wait_ld();
                     }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = use0 ? __uint_as_float(x[e]) * c0 : 0.f;
+                    for (int e = 0; e < 16; ++e) {
+                        asm volatile("" : "+r"(x[e]));
+                        v[e] = use0 ? __uint_as_float(x[e]) * c0 : 0.f;
+                    }
                     if (use1) {
-                        dev::tmem_ld32(tmem + lane_base + L::kColO + D + c, x);
+                        dev::tmem_ld16(tmem + lane_base + L::kColO + D + c, x);
                         dev::tc_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = fmaf(__uint_as_float(x[e]), c1, v[e]);
+                        for (int e = 0; e < 16; ++e) {
+                            asm volatile("" : "+r"(x[e]));
+                            v[e] = fmaf(__uint_as_float(x[e]), c1, v[e]);
+                        }
                     }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) finite = fmaf(v[e], 0.f, finite);
+                    for (int e = 0; e < 16; ++e) finite = fmaf(v[e], 0.f, finite);
                     if (mine) {
                         if (whole) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8)
+                            for (int e = 0; e < 16; e += 8)
                                 *reinterpret_cast<uint4*>(bo + c + e) =
                                     make_uint4(dev::pack_bf16x2(v[e], v[e + 1]), dev::pack_bf16x2(v[e + 2], v[e + 3]),
                                                dev::pack_bf16x2(v[e + 4], v[e + 5]), dev::pack_bf16x2(v[e + 6], v[e + 7]));
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4)
+                            for (int e = 0; e < 16; e += 4)
                                 *reinterpret_cast<float4*>(po + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                         }
                     }
@@ -584,11 +608,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     again &= again - 1;
                     const int ri = t * 128 + quarter * 32 + src;
                     const int64_t r_out = __shfl_sync(0xffffffffu, orow, src), r_part = __shfl_sync(0xffffffffu, prow, src);
-                    const int32_t s2 = w.it.row0 + ri;
+                    int32_t qh2;
+                    const int32_t tok2 = row_token(a, w.it, ri, qh2);
                     float o[D / 32], m, ls;
-                    exact_row<D>(a, w.it.req, w.it.head,
-                                 a.q + (int64_t)(w.it.q0 + s2 / a.G) * a.q_stride + (w.it.head * a.G + s2 % a.G) * D,
-                                 w.it.tok0, row_limit(w.it, ri, a.G), o, m, ls);
+                    exact_row<D>(a, w.it.req, w.it.head, a.q + (int64_t)tok2 * a.q_stride + qh2 * D, w.it.tok0,
+                                 row_limit(a, w.it, ri), o, m, ls);
                     const float scale = ls == 0.f ? 0.f : 1.f / ls;
                     __syncwarp();
 #pragma unroll
@@ -746,22 +770,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (x == 0 && n_tile[t]) wait(&o_free[t], (n_tile[t] - 1) & 1);
                             const uint64_t bd0 = v_desc + ((s * L::kKV) >> 4);
                             const uint32_t d = tmem + L::kColO + t * D, p = tmem + L::kColP + t * 64;
-                            wait(&p_half[t], c[t] & 1);
-                            if (!ok) break;
-                            dev::tc_fence_after();
-                            if (elect_one()) {
-#pragma unroll
-                                for (int k = 0; k < kStage / 32; ++k)
-                                    dev::tc_mma_ts(d, p + k * 8, bd0 + k * (16 * 128 / 16), idesc, (x == 0 && k == 0) ? 0u : 1u);
-                            }
-                            __syncwarp();
                             wait(&p_full[t], c[t] & 1);
                             if (!ok) break;
                             dev::tc_fence_after();
                             if (elect_one()) {
 #pragma unroll
-                                for (int k = kStage / 32; k < kStage / 16; ++k)
-                                    dev::tc_mma_ts(d, p + k * 8, bd0 + k * (16 * 128 / 16), idesc, 1u);
+                                for (int k = 0; k < kStage / 16; ++k)
+                                    dev::tc_mma_ts(d, p + k * 8, bd0 + k * (16 * 128 / 16), idesc, (x == 0 && k == 0) ? 0u : 1u);
                                 dev::tc_commit(&pv_done[t]);
                                 if (x + 1 == ns_t) dev::tc_commit(&o_full[t]);
                             }
@@ -835,8 +850,8 @@ __global__ void __launch_bounds__(kMergeThreads) k_chunk_merge(ChunkArgs a, cons
             }
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int32_t sr = cut.row0 + row;
-        const int64_t orow = (int64_t)(cut.q0 + sr / a.G) * a.Hq + cut.head * a.G + sr % a.G;
+        const int32_t x = cut.rem + row, t = over_g(a, x);
+        const int64_t orow = (int64_t)(cut.q0 + t) * a.Hq + cut.head * a.G + x - t * a.G;
         uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + orow * D + lane * E);
 #pragma unroll
         for (int e = 0; e < E; e += 2) dst[e / 2] = dev::pack_bf16x2(o[e] * inv, o[e + 1] * inv);
@@ -845,7 +860,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_chunk_merge(ChunkArgs a, cons
 }
 
 template <int D>
-cudaError_t launch_chunk(const ChunkArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, cudaStream_t stream) {
+cudaError_t launch_chunk(const ChunkArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq, int ctas, cudaStream_t stream) {
     using L = Layout<D>;
     // setmaxnreg hands out what the block was launched with: it has to have been 128 a thread
     static const cudaError_t ready = [] {
@@ -857,7 +872,7 @@ cudaError_t launch_chunk(const ChunkArgs& a, const CUtensorMap& tk, const CUtens
     if (ready != cudaSuccess) return ready;
     cudaError_t e = cudaFuncSetAttribute(k_chunk<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
-    k_chunk<D><<<ctas, kThreads, L::kAlloc, stream>>>(a, tk, tv);
+    k_chunk<D><<<ctas, kThreads, L::kAlloc, stream>>>(a, tk, tv, tq);
     return cudaGetLastError();
 }
 
@@ -901,9 +916,13 @@ extern "C" fca_status fca_chunk_attention(const void* q, int64_t q_row_stride, c
     a.Hq = plan->Hq;
     a.Hkv = plan->Hkv;
     a.G = plan->G;
+    a.div_g = (65536u + plan->G - 1) / plan->G;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = plan->dev_status;
-    const cudaError_t e = plan->D == 128 ? launch_chunk<128>(a, tk, tv, plan->ctas, s) : launch_chunk<64>(a, tk, tv, plan->ctas, s);
+    CUtensorMap tq = tk;
+    a.q_tma = 128 % plan->G == 0;
+    if (a.q_tma && !make_rows_map(&tq, q, plan->T, plan->Hq, plan->D, q_row_stride, plan->G, 128 / plan->G)) return FCA_ERR_CUDA;
+    const cudaError_t e = plan->D == 128 ? launch_chunk<128>(a, tk, tv, tq, plan->ctas, s) : launch_chunk<64>(a, tk, tv, tq, plan->ctas, s);
     if (note_cuda(e) != cudaSuccess) return FCA_ERR_CUDA;
     if (plan->may_cut) {
         const dim3 grid(plan->ctas, kMergeSplit);

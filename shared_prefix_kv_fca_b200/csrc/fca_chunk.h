@@ -16,13 +16,13 @@ constexpr int kChunkTileCost = 1;    // a tile's own cost (query load, pipeline 
 constexpr int kChunkMinPiece = 2;    // fewest stages a tile is cut into
 constexpr int kChunkMaxCtas = 256;
 
-// One piece of a tile: stacked rows [row0, row0 + nrows) of request `req` and
-// KV head `head` (row i is query head head * G + i % G of the request's row
-// i / G, which is row q0 + i / G of q) over cached tokens [tok0, tok1).  Row i
-// sees tokens below min(tok1, lim0 + i / G + 1).  A whole tile writes out and lse (slot
-// -1); a piece of a cut tile writes its partial rows to `slot`.
+// One piece of a tile: `nrows` stacked rows of request `req` and KV head `head`
+// over cached tokens [tok0, tok1).  Row i of the tile is row q0 + (rem + i) / G of q,
+// query head head * G + (rem + i) % G, and sees tokens below
+// min(tok1, lim0 + (rem + i) / G + 1).  A whole tile writes out and lse (slot -1); a piece
+// of a cut tile writes its partial rows to `slot`.
 struct ChunkItem {
-    int32_t req, head, q0, row0;
+    int32_t req, head, q0, rem;
     int32_t nrows, tok0, tok1, lim0;
     int32_t slot, pad0, pad1, pad2;
 };
@@ -30,7 +30,7 @@ struct ChunkItem {
 // A tile that was cut: its pieces are in slot 2 * cta0 + 1 and then 2 * c for
 // c in (cta0, cta1].  nrows 0: no record.
 struct ChunkCut {
-    int32_t cta0, cta1, q0, row0;
+    int32_t cta0, cta1, q0, rem;
     int32_t nrows, head, pad0, pad1;
 };
 

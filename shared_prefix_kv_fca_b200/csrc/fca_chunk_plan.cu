@@ -232,10 +232,10 @@ __global__ void __launch_bounds__(kListThreads) k_chunk_lists(ChunkPlanArgs a) {
     ChunkItem it;
     it.req = r;
     it.head = head;
-    it.q0 = q0;
-    it.row0 = (int32_t)row0;
+    it.q0 = q0 + (int32_t)(row0 / G);
+    it.rem = (int32_t)(row0 % G);
     it.nrows = (int32_t)(row1 - row0);
-    it.lim0 = whole ? L : L - n;
+    it.lim0 = whole ? L : L - n + (int32_t)(row0 / G);
     it.pad0 = it.pad1 = it.pad2 = 0;
 
     // Walk the boundaries c Q inside [s, e).  One that would leave a piece under
@@ -271,8 +271,8 @@ __global__ void __launch_bounds__(kListThreads) k_chunk_lists(ChunkPlanArgs a) {
         ChunkCut cut;
         cut.cta0 = first_cut - 1;
         cut.cta1 = last_cut;
-        cut.q0 = q0;
-        cut.row0 = it.row0;
+        cut.q0 = it.q0;
+        cut.rem = it.rem;
         cut.nrows = it.nrows;
         cut.head = head;
         cut.pad0 = cut.pad1 = 0;

@@ -116,6 +116,10 @@ cudaError_t note_cuda(cudaError_t e);
 
 // TMA descriptor of a K or V cache [num_blocks * 16][Hkv][D] bf16 (fca_api.cu).
 bool make_cache_map(CUtensorMap* map, const void* base, int32_t num_blocks, int32_t Hkv, int32_t D);
+// ... and of rows [rows][heads][D] bf16 that are row_stride elements apart, in boxes of 64 elements x
+// box_heads x box_rows.
+bool make_rows_map(CUtensorMap* map, const void* base, int32_t rows, int32_t heads, int32_t D, int64_t row_stride,
+                   int32_t box_heads, int32_t box_rows);
 
 // The memory pool plans allocate from, on the current device (fca_plan.cu).
 cudaError_t plan_pool(cudaMemPool_t* out);
