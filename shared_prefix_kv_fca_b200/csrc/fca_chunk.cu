@@ -19,15 +19,14 @@
 //     the cache's bytes, and the softmax of a stage (a row is one thread) takes
 //     longer than its bytes.
 //
-// 512 threads:
-//   warps 0-3, 4-7  softmax of tile 0 and tile 1, one thread a row: the scores
-//                of a stage are read from tensor memory into registers, the
-//                weights go back as bf16 over them in two halves, and the
-//                accumulator is rescaled in place in the rare case that the row's
-//                maximum outgrows its reference;
-//   warps 8-11   query loads and epilogue;
-//   warps 12, 13 TMA loads of K and V, one block of 16 tokens a box;
-//   warps 14, 15 MMA issue: S = Q K^T (operands in shared memory), and
+// 384 threads:
+//   warps 0-3, 4-7  the warpgroups of tile 0 and tile 1, one thread a row: load the
+//                tile's queries, then for each stage read the scores from tensor memory
+//                into registers and write the weights back as bf16; the
+//                accumulator is rescaled in place in the rare case that a row's maximum
+//                outgrows its reference; at the item's end they normalise and store;
+//   warps 8, 9   TMA loads of K and V, one block of 16 tokens a box;
+//   warps 10, 11 MMA issue: S = Q K^T (operands in shared memory), and
 //                O += P V (P from tensor memory).
 // Tensor memory holds one score buffer, two weight buffers and two
 // accumulators.  The tiles take turns with the scores: a softmax warp copies its
@@ -51,12 +50,12 @@ namespace {
 
 constexpr int kStage = kChunkStage;
 constexpr int kBlkPerStage = kStage / kBlockSize;
-constexpr int kThreads = 512;
-constexpr int kEpiWarp0 = 8;
-constexpr int kKWarp = 12, kVWarp = 13, kQKWarp = 14;
-// Registers a thread: the four warpgroups' shares add up to the launch's 128 each.
-constexpr int kRegsSoftmax = 184, kRegsEpilogue = 88, kRegsOthers = 56;
-static_assert(2 * kRegsSoftmax + kRegsEpilogue + kRegsOthers == 4 * 128, "register shares");
+constexpr int kThreads = 384;
+constexpr int kKWarp = 8, kVWarp = 9, kQKWarp = 10;
+// Registers a thread: the three warpgroups' shares add up to the launch's.
+constexpr int kRegsLaunch = 168;
+constexpr int kRegsTile = 208, kRegsOthers = 88;
+static_assert(2 * kRegsTile + kRegsOthers == 3 * kRegsLaunch, "register shares");
 // A row's exponentials are taken against a reference that follows its running
 // maximum only when that is 2^8 above it: the accumulator is rescaled in few stages, and
 // weights up to 2^8 are as exact in bf16 and fp32 as those up to 1.
@@ -94,9 +93,9 @@ struct Layout {
     static constexpr int kOffQ = 0;                      // two tiles
     static constexpr int kOffK = kOffQ + 2 * kTileQ;
     static constexpr int kOffV = kOffK + kKSlots * kKV;
-    static constexpr int kOffML = kOffV + kVSlots * kKV; // [2][2][128] f32: a row's reference and sum
-    static constexpr int kOffBar = kOffML + 2 * 2 * 128 * 4;
-    static constexpr int kNumBars = 2 * (kKSlots + kVSlots) + 9 * 2 + 2;
+    static constexpr int kOffML = kOffV + kVSlots * kKV; // [2][128] f32: tile 1's row references and sums, for tile 0
+    static constexpr int kOffBar = kOffML + 2 * 128 * 4;
+    static constexpr int kNumBars = 2 * (kKSlots + kVSlots) + 5 * 2 + 4;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
     static constexpr int kAlloc = kOffMisc + 32;
     static constexpr uint32_t kColS = 0;                 // scores: 128 fp32 columns
@@ -274,11 +273,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* s_free = s_full + 2;             // ... and copied
     uint64_t* p_full = s_free + 1;             // [2] the tile's weights are written
     uint64_t* pv_done = p_full + 2;            // [2] the P V reading them has completed
-    uint64_t* o_full = pv_done + 2;            // [2] an item's last P V of the tile has completed
-    uint64_t* o_free = o_full + 2;             // [2] the epilogue has read the accumulator
-    uint64_t* ml_full = o_free + 2;            // [2] the tile's row state is written
-    uint64_t* ml_free = ml_full + 2;           // [2] ... and read
-    uint64_t* mma_done = ml_free + 2;
+    uint64_t* x_full = pv_done + 2;            // tile 1's row state of a dual item is written
+    uint64_t* x_free = x_full + 1;             // ... and it and the accumulator are read
+    uint64_t* mma_done = x_free + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 16);
     float* ml = reinterpret_cast<float*>(smem + L::kOffML);
@@ -299,12 +296,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             dev::mbar_init(&s_full[t], 1);
             dev::mbar_init(&p_full[t], 128);
             dev::mbar_init(&pv_done[t], 1);
-            dev::mbar_init(&o_full[t], 1);
-            dev::mbar_init(&o_free[t], 128);
-            dev::mbar_init(&ml_full[t], 128);
-            dev::mbar_init(&ml_free[t], 128);
         }
         dev::mbar_init(s_free, 128);
+        dev::mbar_init(x_full, 128);
+        dev::mbar_init(x_free, 128);
         dev::mbar_init(mma_done, 2);
         *abort_flag = 0;
         dev::fence_mbarrier_init();
@@ -318,34 +313,74 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp < kEpiWarp0) {
-        // ------------------------------------------------ softmax
-        regs_inc<kRegsSoftmax>();
+    if (warp < kKWarp) {
+        // ------------------------------------------------ a tile's warpgroup
+        regs_inc<kRegsTile>();
         const int t = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t s_addr = tmem + lane_base + L::kColS, p_addr = tmem + lane_base + L::kColP + t * 64,
                        o_addr = tmem + lane_base + L::kColO + t * D;
         bool ok = true;
-        uint32_t g = 0;                 // stages of this tile so far
-        uint32_t gv = 0;                // stages of the CTA before the item
-        uint32_t n_items = 0;           // items with stages for this tile so far
-        Work nxt = load_work(a, first);
-        for (int32_t i = first; ok && i < last; ++i) {
-            const Work w = nxt;
-            if (i + 1 < last) nxt = load_work(a, i + 1);
-            const int32_t ns = t ? w.ns1 : w.ns0;
-            if (ns == 0) {
-                gv += w.ns;
-                continue;
+        // Queries of tile t for the next item that has some, from item i on (a dual item's go to
+        // tile 0), once the products reading the last ones have completed.
+        uint32_t n_q = 0;
+        auto load_q = [&](int32_t i) {
+            for (; i < last; ++i) {
+                const Work w = load_work(a, i);
+                if (t ? w.dual || w.ns == 0 : w.ns0 == 0) continue;
+                if (n_q && !dev::mbar_wait(&q_free[t], (n_q - 1) & 1, abort_flag, a.err)) ok = false;
+                ++n_q;
+                if (!ok) return;
+                uint8_t* const q_tile = smem + L::kOffQ + t * L::kTileQ;
+                if (a.q_tma) {
+                    // (rows behind the request's are other requests' queries: computed like
+                    // the others and left alone)
+                    if (row == 0) {
+                        dev::mbar_arrive_expect_tx(&q_full[t], L::kTileQ);
+                        for (int hf = 0; hf < L::kHalves; ++hf)
+                            dev::tma_load_3d(q_tile + hf * (128 * 128), &tmQ, &q_full[t], hf * 64, w.it.head * a.G,
+                                             w.it.q0 + over_g(a, t * 128));
+                    }
+                    return;
+                }
+                constexpr int C = D / 8;            // 16-byte chunks a row
+#pragma unroll 4
+                for (int e = row; e < 128 * C; e += 128) {
+                    const int r = e / C, c = e % C, ri = t * 128 + r;
+                    int32_t qhead;
+                    const int32_t tok = row_token(a, w.it, min(ri, w.it.nrows - 1), qhead);
+                    cp_async16(dev::smem_u32(q_tile) + sw128_off(r, c >> 3, c & 7),
+                               a.q + (int64_t)tok * a.q_stride + qhead * D + c * 8, ri < w.it.nrows ? 16u : 0u);
+                }
+                cp_async_wait();
+                dev::fence_proxy_async_smem();
+                dev::mbar_arrive(&q_full[t]);
+                return;
             }
-            const int r_item = w.dual ? row : t * 128 + row;             // stacked row within the item
-            const bool live = (w.dual ? quarter * 32 : t * 128 + quarter * 32) < w.it.nrows;
-            const int32_t lim = row_limit(a, w.it, min(r_item, w.it.nrows - 1)) - w.it.tok0;   // tokens of the item it sees
+        };
+        load_q(first);
+        uint32_t g = 0, g_other = 0;    // stages of this tile, and of the other, before the item
+        uint32_t gv = 0;                // stages of the CTA before the item
+        uint32_t n_dual = 0;            // items joined from both tiles
+        for (int32_t i = first; ok && i < last; ++i) {
+            int32_t ns, ns_other, ns_item, lim, tail;
+            bool dual, live;
+            {   // (only what the stages need is kept: the scores take up the registers)
+                const Work w = load_work(a, i);
+                ns = t ? w.ns1 : w.ns0;
+                ns_other = t ? w.ns0 : w.ns1;
+                ns_item = w.ns;
+                dual = w.dual;
+                const int r_item = w.dual ? row : t * 128 + row;         // stacked row within the item
+                live = (w.dual ? quarter * 32 : t * 128 + quarter * 32) < w.it.nrows;
+                lim = row_limit(a, w.it, min(r_item, w.it.nrows - 1)) - w.it.tok0;   // tokens of the item it sees
+                // the tile whose P V comes first clears the last stage's tail
+                const bool clears = w.it.tok1 % kBlockSize != 0 && (w.dual || t == 0 || w.ns0 < w.ns);
+                tail = clears ? (w.it.tok1 - w.it.tok0) - (w.ns - 1) * kStage : 0;   // valid tokens of that stage
+            }
             float m = -INFINITY, l = 0.f;       // reference (log2 domain) and sum of the weights
-            // the tile whose P V comes first clears the last stage's tail
-            const bool clears = w.it.tok1 % kBlockSize != 0 && (w.dual || t == 0 || w.ns0 < w.ns);
             for (int32_t x = 0; x < ns; ++x, ++g) {
-                const int32_t j = w.dual ? 2 * x + t : x;
+                const int32_t j = dual ? 2 * x + t : x;
                 bool got = dev::mbar_wait(&s_full[t], g & 1, abort_flag, a.err);
                 if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
                 dev::tc_fence_after();
@@ -355,10 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // 0 x NaN is not, so V's rows there are cleared.
                 auto ready = [&](bool waited) -> bool {
                     bool up = waited || g == 0 || dev::mbar_wait(&pv_done[t], (g - 1) & 1, abort_flag, a.err);
-                    if (clears && j == w.ns - 1) {
+                    if (tail && j == ns_item - 1) {
                         const uint32_t s = (gv + j) % L::kVSlots;
                         up = up && dev::mbar_wait(&v_full[s], ((gv + j) / L::kVSlots) & 1, abort_flag, a.err);
-                        const int r0 = w.it.tok1 - w.it.tok0 - j * kStage, r1 = (r0 + kBlockSize - 1) / kBlockSize * kBlockSize;
+                        const int r0 = tail, r1 = (r0 + kBlockSize - 1) / kBlockSize * kBlockSize;
                         uint8_t* vs = smem + L::kOffV + s * L::kKV;
                         for (int e = row; up && e < (r1 - r0) * 8 * L::kHalves; e += 128) {
                             const int rr = r0 + e / (8 * L::kHalves), c = e % (8 * L::kHalves);
@@ -441,198 +476,145 @@ __global__ void __launch_bounds__(kThreads, 1)
                 dev::mbar_arrive(&p_full[t]);
             }
             if (!ok) break;
-            gv += w.ns;
-            // the rows' state for the epilogue, once it has read the last one
-            if (n_items >= 1) {
-                bool got = dev::mbar_wait(&ml_free[t], (n_items - 1) & 1, abort_flag, a.err);
-                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-            }
-            ml[t * 256 + row] = m;
-            ml[t * 256 + 128 + row] = l;
-            dev::mbar_arrive(&ml_full[t]);
-            ++n_items;
-        }
-    } else if (warp < kKWarp) {
-        // ------------------------------------------------ query loads and epilogue
-        regs_dec<kRegsEpilogue>();
-        const int quarter = warp & 3, tid = threadIdx.x - kEpiWarp0 * 32, row = quarter * 32 + lane;
-        const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        const uint32_t q_smem = dev::smem_u32(smem + L::kOffQ);
-        // Query tile b of an item, once the products of the tile's last queries have completed.
-        uint32_t n_q[2] = {0, 0};
-        bool ok = true;
-        auto load_q = [&](const Work& w) {
-            constexpr int C = D / 8;            // 16-byte chunks a row
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (b ? w.dual : w.ns0 == 0) continue;
-                if (n_q[b] && (!a.q_tma || warp == kEpiWarp0)) {
-                    bool got = dev::mbar_wait(&q_free[b], (n_q[b] - 1) & 1, abort_flag, a.err);
-                    if (!__all_sync(0xffffffffu, got)) { ok = false; return; }
-                }
-                ++n_q[b];
-                if (a.q_tma) {
-                    // (a tile's rows behind the request's are other requests' queries: computed
-                    // like the others and left alone)
-                    if (tid == 0) {
-                        dev::mbar_arrive_expect_tx(&q_full[b], L::kTileQ);
-                        for (int hf = 0; hf < L::kHalves; ++hf)
-                            dev::tma_load_3d(smem + L::kOffQ + b * L::kTileQ + hf * (128 * 128), &tmQ, &q_full[b], hf * 64,
-                                             w.it.head * a.G, w.it.q0 + over_g(a, b * 128));
-                    }
-                    continue;
-                }
-#pragma unroll 4
-                for (int e = tid; e < 128 * C; e += 128) {
-                    const int r = e / C, c = e % C, ri = b * 128 + r;
-                    int32_t qhead;
-                    const int32_t tok = row_token(a, w.it, min(ri, w.it.nrows - 1), qhead);
-                    cp_async16(q_smem + b * L::kTileQ + sw128_off(r, c >> 3, c & 7),
-                               a.q + (int64_t)tok * a.q_stride + qhead * D + c * 8, ri < w.it.nrows ? 16u : 0u);
-                }
-                cp_async_wait();
-                dev::fence_proxy_async_smem();
-                dev::mbar_arrive(&q_full[b]);
-            }
-        };
-        uint32_t n0 = 0, n1 = 0;                // items with stages for tile 0, tile 1
-        int32_t qi = first;                     // the item whose queries are loaded next
-        auto load_next = [&](int32_t from) {
-            for (qi = from; qi < last; ++qi) {
-                const Work qw = load_work(a, qi);
-                if (qw.ns) {
-                    load_q(qw);
-                    return;
-                }
-            }
-        };
-        load_next(first);
-        for (int32_t i = first; ok && i < last; ++i) {
-            const Work w = load_work(a, i);
-            if (w.ns) load_next(i + 1);
+            gv += ns_item;
+            g_other += ns_other;
+            if (ns && (t == 0 || !dual)) load_q(i + 1);
             if (!ok) break;
-            // Rows that this warp's threads hold: out and lse, or the piece's partial rows.
-            for (int t = 0; t < (w.dual ? 1 : 2); ++t) {
-                // the tiles whose accumulators make up these rows
-                const bool use0 = t == 0 && w.ns0 > 0, use1 = (t == 1 || w.dual) && w.ns1 > 0;
-                float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-                bool got = true;
-                if (use0) {
-                    got = dev::mbar_wait(&ml_full[0], n0 & 1, abort_flag, a.err);
-                    m0 = ml[row];
-                    l0 = ml[128 + row];
-                    dev::mbar_arrive(&ml_free[0]);
-                    got = got && dev::mbar_wait(&o_full[0], n0 & 1, abort_flag, a.err);
-                    ++n0;
+            const bool join = dual && ns_item > 1;      // both tiles have stages of the same rows
+            if (dual && t == 1) {
+                // tile 0 joins the two accumulators
+                if (join) {
+                    ml[row] = m;
+                    ml[128 + row] = l;
+                    dev::mbar_arrive(x_full);
+                    ok = __all_sync(0xffffffffu, dev::mbar_wait(x_free, n_dual & 1, abort_flag, a.err));
+                    ++n_dual;
                 }
-                if (use1) {
-                    got = got && dev::mbar_wait(&ml_full[1], n1 & 1, abort_flag, a.err);
-                    m1 = ml[256 + row];
-                    l1 = ml[256 + 128 + row];
-                    dev::mbar_arrive(&ml_free[1]);
-                    got = got && dev::mbar_wait(&o_full[1], n1 & 1, abort_flag, a.err);
-                    ++n1;
+                continue;
+            }
+            // ------------------------------------------------ the item's rows
+            const Work w = load_work(a, i);
+            const int r_item = t * 128 + row;
+            const bool mine = r_item < w.it.nrows;
+            float c0, c1 = 0.f, lw;             // coefficients of the accumulators; the row's log2 sum
+            {
+                bool up = ns == 0 || dev::mbar_wait(&pv_done[t], (g - 1) & 1, abort_flag, a.err);
+                float m1 = -INFINITY, l1 = 0.f;
+                if (join) {
+                    up = up && dev::mbar_wait(x_full, n_dual & 1, abort_flag, a.err) &&
+                         dev::mbar_wait(&pv_done[1], (g_other - 1) & 1, abort_flag, a.err);
+                    m1 = ml[row];
+                    l1 = ml[128 + row];
+                    ++n_dual;
                 }
-                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                if (!__all_sync(0xffffffffu, up)) { ok = false; break; }
                 dev::tc_fence_after();
-                const int r_item = t * 128 + row;
-                const bool mine = r_item < w.it.nrows;
-                const float M = fmaxf(m0, m1), Mf = M == -INFINITY ? 0.f : M;
-                const float f0 = dev::ex2(m0 - Mf), f1 = dev::ex2(m1 - Mf);
-                const float l = l0 * f0 + l1 * f1, inv = l == 0.f ? 0.f : 1.f / l;
-                const float c0 = f0 * inv, c1 = f1 * inv;
-                int32_t qhead;
-                const int32_t tok = row_token(a, w.it, r_item, qhead);
-                const int64_t orow = (int64_t)tok * a.Hq + qhead;
-                const int64_t prow = (int64_t)w.it.slot * a.part_rows + r_item;
-                float* const po = a.part_o + prow * D;
-                __nv_bfloat16* const bo = a.out + orow * D;
-                const bool whole = w.it.slot < 0;
-                float finite = 0.f;             // NaN once an element is not finite
+                const float M = fmaxf(m, m1), Mf = M == -INFINITY ? 0.f : M;
+                const float f0 = dev::ex2(m - Mf), f1 = dev::ex2(m1 - Mf);
+                const float sum = l * f0 + l1 * f1, inv = sum == 0.f ? 0.f : 1.f / sum;
+                c0 = f0 * inv;
+                c1 = f1 * inv;
+                lw = M + log2f(sum);            // -inf for a row that saw nothing
+            }
+            int32_t qhead;
+            const int32_t tok = row_token(a, w.it, r_item, qhead);
+            const int64_t orow = (int64_t)tok * a.Hq + qhead;
+            const int64_t prow = (int64_t)w.it.slot * a.part_rows + r_item;
+            const bool whole = w.it.slot < 0;
+            float finite = 0.f;                 // NaN once an element is not finite
 #pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                    float v[16];
-                    uint32_t x[16];
-                    if (use0) {
-                        dev::tmem_ld16(tmem + lane_base + L::kColO + c, x);
+            for (int c = 0; c < D; c += 32) {
+                float v[32];
+                {
+                    uint32_t y[32];
+                    if (ns) {
+                        dev::tmem_ld32(o_addr + c, y);
                         dev::tc_wait_ld();
                     }
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        asm volatile("" : "+r"(x[e]));
-                        v[e] = use0 ? __uint_as_float(x[e]) * c0 : 0.f;
-                    }
-                    if (use1) {
-                        dev::tmem_ld16(tmem + lane_base + L::kColO + D + c, x);
-                        dev::tc_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            asm volatile("" : "+r"(x[e]));
-                            v[e] = fmaf(__uint_as_float(x[e]), c1, v[e]);
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) finite = fmaf(v[e], 0.f, finite);
-                    if (mine) {
-                        if (whole) {
-#pragma unroll
-                            for (int e = 0; e < 16; e += 8)
-                                *reinterpret_cast<uint4*>(bo + c + e) =
-                                    make_uint4(dev::pack_bf16x2(v[e], v[e + 1]), dev::pack_bf16x2(v[e + 2], v[e + 3]),
-                                               dev::pack_bf16x2(v[e + 4], v[e + 5]), dev::pack_bf16x2(v[e + 6], v[e + 7]));
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 16; e += 4)
-                                *reinterpret_cast<float4*>(po + c + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-                        }
+                    for (int e = 0; e < 32; ++e) {
+                        asm volatile("" : "+r"(y[e]));
+                        v[e] = ns ? as_f(y[e]) * c0 : 0.f;
                     }
                 }
-                if (use0 || use1) {
-                    dev::tc_fence_before();
-                    if (use0) dev::mbar_arrive(&o_free[0]);
-                    if (use1) dev::mbar_arrive(&o_free[1]);
+                if (join) {
+                    uint32_t y[32];
+                    dev::tmem_ld32(o_addr + D + c, y);
+                    dev::tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        asm volatile("" : "+r"(y[e]));
+                        v[e] = fmaf(as_f(y[e]), c1, v[e]);
+                    }
+                    if (c + 32 == D) {
+                        dev::tc_fence_before();
+                        dev::mbar_arrive(x_free);
+                    }
                 }
-                const float lw = M + log2f(l);      // -inf for a row that saw nothing
+#pragma unroll
+                for (int e = 0; e < 32; ++e) finite = fmaf(v[e], 0.f, finite);
                 if (mine) {
-                    if (!whole)
-                        a.part_w[prow] = lw;
-                    else if (a.lse)
-                        a.lse[orow] = lw * kLn2;
-                }
-                // A product of weight 0 with an inf or NaN that the row does not see
-                // (a later token's) is NaN: rows that are not finite are computed
-                // again from the tokens that they do see.
-                uint32_t again = __ballot_sync(0xffffffffu, mine && isnan(finite));
-                while (again) {
-                    const int src = __ffs(again) - 1;
-                    again &= again - 1;
-                    const int ri = t * 128 + quarter * 32 + src;
-                    const int64_t r_out = __shfl_sync(0xffffffffu, orow, src), r_part = __shfl_sync(0xffffffffu, prow, src);
-                    int32_t qh2;
-                    const int32_t tok2 = row_token(a, w.it, ri, qh2);
-                    float o[D / 32], m, ls;
-                    exact_row<D>(a, w.it.req, w.it.head, a.q + (int64_t)tok2 * a.q_stride + qh2 * D, w.it.tok0,
-                                 row_limit(a, w.it, ri), o, m, ls);
-                    const float scale = ls == 0.f ? 0.f : 1.f / ls;
-                    __syncwarp();
+                    if (whole) {
+                        __nv_bfloat16* const bo = a.out + orow * D + c;
 #pragma unroll
-                    for (int e = 0; e < D / 32; ++e) {
-                        const int col = lane * (D / 32) + e;
-                        if (whole)
-                            a.out[r_out * D + col] = __float2bfloat16(o[e] * scale);
-                        else
-                            a.part_o[r_part * D + col] = o[e] * scale;
-                    }
-                    if (lane == 0) {
-                        const float lr = m + log2f(ls);
-                        if (!whole)
-                            a.part_w[r_part] = lr;
-                        else if (a.lse)
-                            a.lse[r_out] = lr * kLn2;
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4*>(bo + e) =
+                                make_uint4(dev::pack_bf16x2(v[e], v[e + 1]), dev::pack_bf16x2(v[e + 2], v[e + 3]),
+                                           dev::pack_bf16x2(v[e + 4], v[e + 5]), dev::pack_bf16x2(v[e + 6], v[e + 7]));
+                    } else {
+                        float* const po = a.part_o + prow * D + c;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(po + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                     }
                 }
             }
+            dev::tc_fence_before();             // (the next item's weights, and so its P V, come behind this)
+            if (mine) {
+                if (!whole)
+                    a.part_w[prow] = lw;
+                else if (a.lse)
+                    a.lse[orow] = lw * kLn2;
+            }
+            // A product of weight 0 with an inf or NaN that the row does not see
+            // (a later token's) is NaN: rows that are not finite are computed
+            // again from the tokens that they do see.
+            uint32_t again = __ballot_sync(0xffffffffu, mine && isnan(finite));
+            while (again) {
+                const int src = __ffs(again) - 1;
+                again &= again - 1;
+                const int ri = t * 128 + quarter * 32 + src;
+                const int64_t r_out = __shfl_sync(0xffffffffu, orow, src), r_part = __shfl_sync(0xffffffffu, prow, src);
+                int32_t qh2;
+                const int32_t tok2 = row_token(a, w.it, ri, qh2);
+                float o[D / 32], me, le;
+                exact_row<D>(a, w.it.req, w.it.head, a.q + (int64_t)tok2 * a.q_stride + qh2 * D, w.it.tok0,
+                             row_limit(a, w.it, ri), o, me, le);
+                const float scale = le == 0.f ? 0.f : 1.f / le;
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) {
+                    const int col = lane * (D / 32) + e;
+                    if (whole)
+                        a.out[r_out * D + col] = __float2bfloat16(o[e] * scale);
+                    else
+                        a.part_o[r_part * D + col] = o[e] * scale;
+                }
+                if (lane == 0) {
+                    const float lr = me + log2f(le);
+                    if (!whole)
+                        a.part_w[r_part] = lr;
+                    else if (a.lse)
+                        a.lse[r_out] = lr * kLn2;
+                }
+            }
         }
+        if (a.q_tma && row == 0 && n_q) {
+            // never leave with a copy in flight
+            volatile int never = 0;
+            dev::mbar_wait(&q_full[t], (n_q - 1) & 1, &never, a.err);
+        }
+        __syncwarp();
     } else {
         regs_dec<kRegsOthers>();
         if (warp == kKWarp || warp == kVWarp) {
@@ -754,7 +736,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 constexpr uint32_t idesc = dev::idesc_bf16_f32(128, D, false, true);
                 const uint64_t v_desc = dev::smem_desc_sw128(dev::smem_u32(smem + L::kOffV), kStage * 128, 1024);
                 uint32_t c[2] = {0, 0};         // P V so far, by tile
-                uint32_t n_tile[2] = {0, 0};    // items finished, by tile
                 for (int32_t i = first; ok && i < last; ++i) {
                     const Work w = nxt;
                     if (i + 1 < last) nxt = load_work(a, i + 1);
@@ -765,9 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             if (w.dual ? (j & 1) != t : (t == 0 && j >= w.ns0)) continue;
-                            const int32_t x = w.dual ? j >> 1 : j, ns_t = t ? w.ns1 : w.ns0;
-                            // a new item's accumulator starts once the epilogue has read the last one's
-                            if (x == 0 && n_tile[t]) wait(&o_free[t], (n_tile[t] - 1) & 1);
+                            const int32_t x = w.dual ? j >> 1 : j;
                             const uint64_t bd0 = v_desc + ((s * L::kKV) >> 4);
                             const uint32_t d = tmem + L::kColO + t * D, p = tmem + L::kColP + t * 64;
                             wait(&p_full[t], c[t] & 1);
@@ -778,10 +757,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int k = 0; k < kStage / 16; ++k)
                                     dev::tc_mma_ts(d, p + k * 8, bd0 + k * (16 * 128 / 16), idesc, (x == 0 && k == 0) ? 0u : 1u);
                                 dev::tc_commit(&pv_done[t]);
-                                if (x + 1 == ns_t) dev::tc_commit(&o_full[t]);
                             }
                             __syncwarp();
-                            if (x + 1 == ns_t) ++n_tile[t];
                             ++c[t];
                         }
                         if (!ok) break;
@@ -862,12 +839,11 @@ __global__ void __launch_bounds__(kMergeThreads) k_chunk_merge(ChunkArgs a, cons
 template <int D>
 cudaError_t launch_chunk(const ChunkArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq, int ctas, cudaStream_t stream) {
     using L = Layout<D>;
-    // setmaxnreg hands out what the block was launched with: it has to have been 128 a thread
+    // setmaxnreg hands out what the block was launched with: it has to have been kRegsLaunch a thread
     static const cudaError_t ready = [] {
         cudaFuncAttributes at{};
-        cudaError_t e = cudaFuncGetAttributes(&at, k_chunk<D>);
-        if (e == cudaSuccess && at.numRegs != 128) e = cudaErrorInvalidConfiguration;
-        return e;
+        cudaError_t r = cudaFuncGetAttributes(&at, k_chunk<D>);
+        return r == cudaSuccess && at.numRegs != kRegsLaunch ? cudaErrorInvalidConfiguration : r;
     }();
     if (ready != cudaSuccess) return ready;
     cudaError_t e = cudaFuncSetAttribute(k_chunk<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
