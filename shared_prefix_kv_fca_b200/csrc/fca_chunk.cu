@@ -34,7 +34,7 @@
 // anything, so that the other tile's Q K^T, and this tile's next, never wait for an
 // exponential or a P V, and scores are there when a tile has finished a stage.
 // (With a score buffer per tile and the weights written over the scores, a tile's next
-// Q K^T had to wait for its P V: 5300 cycles a stage of 256 x 128 instead of TODO.)
+// Q K^T had to wait for its P V: 5300 cycles a stage of 256 x 128 instead of 3100.)
 // Every wait is bounded (fca_device.cuh); a role that gives up sets the CTA's
 // abort flag, the others leave at their next wait, copies and MMAs in flight
 // are waited for, and tensor memory is freed.
@@ -191,12 +191,6 @@ __device__ __forceinline__ void wait_ld(uint32_t (&x)[32], uint32_t (&y)[32]) {
 
 __device__ __forceinline__ float as_f(uint32_t x) { return __uint_as_float(x); }
 
-// Columns c .. c + 31 of a row from nv on to -inf.
-__device__ __forceinline__ void mask32(uint32_t (&x)[32], int c, int nv) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = c + i < nv ? x[i] : 0xff800000u;
-}
-
 __device__ __forceinline__ void max32(const uint32_t (&x)[32], float& a, float& b) {
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
@@ -321,36 +315,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_addr = tmem + lane_base + L::kColS, p_addr = tmem + lane_base + L::kColP + t * 64,
                        o_addr = tmem + lane_base + L::kColO + t * D;
         bool ok = true;
-        // Queries of tile t for the next item that has some, from item i on (a dual item's go to
+        // Where the head group does not divide a tile (else the V warp loads the queries by TMA):
+        // queries of tile t for the next item that has some, from item i on (a dual item's go to
         // tile 0), once the products reading the last ones have completed.
         uint32_t n_q = 0;
         auto load_q = [&](int32_t i) {
+            if (a.q_tma) return;
             for (; i < last; ++i) {
                 const Work w = load_work(a, i);
                 if (t ? w.dual || w.ns == 0 : w.ns0 == 0) continue;
                 if (n_q && !dev::mbar_wait(&q_free[t], (n_q - 1) & 1, abort_flag, a.err)) ok = false;
                 ++n_q;
                 if (!ok) return;
-                uint8_t* const q_tile = smem + L::kOffQ + t * L::kTileQ;
-                if (a.q_tma) {
-                    // (rows behind the request's are other requests' queries: computed like
-                    // the others and left alone)
-                    if (row == 0) {
-                        dev::mbar_arrive_expect_tx(&q_full[t], L::kTileQ);
-                        for (int hf = 0; hf < L::kHalves; ++hf)
-                            dev::tma_load_3d(q_tile + hf * (128 * 128), &tmQ, &q_full[t], hf * 64, w.it.head * a.G,
-                                             w.it.q0 + over_g(a, t * 128));
-                    }
-                    return;
-                }
                 constexpr int C = D / 8;            // 16-byte chunks a row
+                const uint32_t q_tile = dev::smem_u32(smem + L::kOffQ) + t * L::kTileQ;
 #pragma unroll 4
                 for (int e = row; e < 128 * C; e += 128) {
                     const int r = e / C, c = e % C, ri = t * 128 + r;
                     int32_t qhead;
                     const int32_t tok = row_token(a, w.it, min(ri, w.it.nrows - 1), qhead);
-                    cp_async16(dev::smem_u32(q_tile) + sw128_off(r, c >> 3, c & 7),
-                               a.q + (int64_t)tok * a.q_stride + qhead * D + c * 8, ri < w.it.nrows ? 16u : 0u);
+                    cp_async16(q_tile + sw128_off(r, c >> 3, c & 7), a.q + (int64_t)tok * a.q_stride + qhead * D + c * 8,
+                               ri < w.it.nrows ? 16u : 0u);
                 }
                 cp_async_wait();
                 dev::fence_proxy_async_smem();
@@ -363,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t gv = 0;                // stages of the CTA before the item
         uint32_t n_dual = 0;            // items joined from both tiles
         for (int32_t i = first; ok && i < last; ++i) {
-            int32_t ns, ns_other, ns_item, lim, tail;
+            int32_t ns, ns_other, ns_item, lim, n_hot;
             bool dual, live;
             {   // (only what the stages need is kept: the scores take up the registers)
                 const Work w = load_work(a, i);
@@ -374,41 +359,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int r_item = w.dual ? row : t * 128 + row;         // stacked row within the item
                 live = (w.dual ? quarter * 32 : t * 128 + quarter * 32) < w.it.nrows;
                 lim = row_limit(a, w.it, min(r_item, w.it.nrows - 1)) - w.it.tok0;   // tokens of the item it sees
-                // the tile whose P V comes first clears the last stage's tail
-                const bool clears = w.it.tok1 % kBlockSize != 0 && (w.dual || t == 0 || w.ns0 < w.ns);
-                tail = clears ? (w.it.tok1 - w.it.tok0) - (w.ns - 1) * kStage : 0;   // valid tokens of that stage
+                // stages of which every row of this warp sees all
+                const int32_t all = max(0, __reduce_min_sync(0xffffffffu, lim)) / kStage;
+                n_hot = min(ns, w.dual ? (all - t + 1) >> 1 : all);
             }
             float m = -INFINITY, l = 0.f;       // reference (log2 domain) and sum of the weights
-            for (int32_t x = 0; x < ns; ++x, ++g) {
+            // Before a stage's first weights: the P V of the tile's stage before has read
+            // the last ones.
+            auto weights_free = [&]() -> bool {
+                const bool up = g == 0 || dev::mbar_wait(&pv_done[t], (g - 1) & 1, abort_flag, a.err);
+                dev::tc_fence_after();
+                return __all_sync(0xffffffffu, up);
+            };
+            // Stage x.  In an edge stage (x >= n_hot) some row of the warp does not see all
+            // 128 columns: those are set to -inf where they lie first, in a short loop, so that
+            // the stage itself is one body of code for all (instructions that run once
+            // an item come from far: a second body with masks cost 3500 cycles an item).
+            auto stage = [&](int32_t x) -> bool {
                 const int32_t j = dual ? 2 * x + t : x;
                 bool got = dev::mbar_wait(&s_full[t], g & 1, abort_flag, a.err);
-                if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+                if (!__all_sync(0xffffffffu, got)) return false;
                 dev::tc_fence_after();
-                // Before the stage's first weights: the P V of the tile's stage before has
-                // read the last ones.  And the last block's slots behind the range were
-                // loaded too and may hold anything, NaN included: their weights are 0, but
-                // 0 x NaN is not, so V's rows there are cleared.
-                auto ready = [&](bool waited) -> bool {
-                    bool up = waited || g == 0 || dev::mbar_wait(&pv_done[t], (g - 1) & 1, abort_flag, a.err);
-                    if (tail && j == ns_item - 1) {
-                        const uint32_t s = (gv + j) % L::kVSlots;
-                        up = up && dev::mbar_wait(&v_full[s], ((gv + j) / L::kVSlots) & 1, abort_flag, a.err);
-                        const int r0 = tail, r1 = (r0 + kBlockSize - 1) / kBlockSize * kBlockSize;
-                        uint8_t* vs = smem + L::kOffV + s * L::kKV;
-                        for (int e = row; up && e < (r1 - r0) * 8 * L::kHalves; e += 128) {
-                            const int rr = r0 + e / (8 * L::kHalves), c = e % (8 * L::kHalves);
-                            *reinterpret_cast<uint4*>(vs + sw128_off(rr, c >> 3, c & 7)) = make_uint4(0, 0, 0, 0);
+                if (x >= n_hot) {
+                    const int nv = lim - j * kStage;             // columns that the row sees
+                    const int low = __reduce_min_sync(0xffffffffu, nv), high = __reduce_max_sync(0xffffffffu, nv);
+#pragma unroll 1
+                    for (int c = max(0, low) / 16 * 16; c < kStage; c += 16) {
+                        uint32_t y[16];
+                        if (c < high) {
+                            dev::tmem_ld16(s_addr + c, y);
+                            dev::tc_wait_ld();
                         }
-                        dev::fence_proxy_async_smem();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            asm volatile("" : "+r"(y[e]));
+                            y[e] = c + e < nv ? y[e] : 0xff800000u;
+                        }
+                        dev::tmem_st16(s_addr + c, y);
                     }
-                    dev::tc_fence_after();
-                    return __all_sync(0xffffffffu, up);
-                };
-                if (!live) {
-                    dev::mbar_arrive(s_free);
-                    if (!ready(false)) { ok = false; break; }
-                    dev::mbar_arrive(&p_full[t]);
-                    continue;
+                    dev::tc_wait_st();
                 }
                 uint32_t s0[32], s1[32], s2[32], s3[32];
                 dev::tmem_ld32(s_addr, s0);
@@ -419,13 +408,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait_ld(s2, s3);
                 dev::tc_fence_before();
                 dev::mbar_arrive(s_free);
-                const int nv = lim - j * kStage;                 // columns that the row sees
-                if (__any_sync(0xffffffffu, nv < kStage)) {
-                    mask32(s0, 0, nv);
-                    mask32(s1, 32, nv);
-                    mask32(s2, 64, nv);
-                    mask32(s3, 96, nv);
-                }
                 float mx = -INFINITY, my = -INFINITY, mz = -INFINITY, mw = -INFINITY;
                 max32(s0, mx, my);
                 max32(s1, mz, mw);
@@ -438,13 +420,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l *= f;
                     m = mx;
                 }
-                bool waited = false;
                 // (an item's first P V overwrites the accumulator)
                 if (x > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-                    got = dev::mbar_wait(&pv_done[t], (g - 1) & 1, abort_flag, a.err);
-                    if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-                    waited = true;
-                    dev::tc_fence_after();
+                    if (!weights_free()) return false;           // that P V has brought the accumulator up to date
 #pragma unroll 1
                     for (int c = 0; c < D / 16; ++c) {
                         uint32_t ov[16];
@@ -464,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t p[32];
                 weights32(s0, sc, nm, p, sum);
                 weights32(s1, sc, nm, p + 16, sum2);
-                if (!ready(waited)) { ok = false; break; }
+                if (!weights_free()) return false;
                 dev::tmem_st32(p_addr, p);
                 weights32(s2, sc, nm, p, sum);
                 weights32(s3, sc, nm, p + 16, sum2);
@@ -474,6 +452,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 dev::tc_wait_st();
                 dev::tc_fence_before();
                 dev::mbar_arrive(&p_full[t]);
+                return true;
+            };
+            int32_t x = 0;
+            if (live) {
+#pragma unroll 1
+                for (; ok && x < ns; ++x, ++g) ok = stage(x);
+            } else {
+                // rows that do not exist: the barriers only
+#pragma unroll 1
+                for (; ok && x < ns; ++x, ++g) {
+                    ok = __all_sync(0xffffffffu, dev::mbar_wait(&s_full[t], g & 1, abort_flag, a.err));
+                    if (!ok) break;
+                    dev::mbar_arrive(s_free);
+                    ok = weights_free();
+                    if (ok) dev::mbar_arrive(&p_full[t]);
+                }
             }
             if (!ok) break;
             gv += ns_item;
@@ -523,48 +517,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool whole = w.it.slot < 0;
             float finite = 0.f;                 // NaN once an element is not finite
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float v[32];
-                {
-                    uint32_t y[32];
-                    if (ns) {
-                        dev::tmem_ld32(o_addr + c, y);
-                        dev::tc_wait_ld();
-                    }
+            for (int c = 0; c < D / 16; ++c) {
+                float v[16];
+                uint32_t y[16];
+                if (ns) {
+                    dev::tmem_ld16(o_addr + 16 * c, y);
+                    dev::tc_wait_ld();
+                }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        asm volatile("" : "+r"(y[e]));
-                        v[e] = ns ? as_f(y[e]) * c0 : 0.f;
-                    }
+                for (int e = 0; e < 16; ++e) {
+                    asm volatile("" : "+r"(y[e]));
+                    v[e] = ns ? as_f(y[e]) * c0 : 0.f;
                 }
                 if (join) {
-                    uint32_t y[32];
-                    dev::tmem_ld32(o_addr + D + c, y);
+                    uint32_t z[16];
+                    dev::tmem_ld16(o_addr + D + 16 * c, z);
                     dev::tc_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        asm volatile("" : "+r"(y[e]));
-                        v[e] = fmaf(as_f(y[e]), c1, v[e]);
+                    for (int e = 0; e < 16; ++e) {
+                        asm volatile("" : "+r"(z[e]));
+                        v[e] = fmaf(as_f(z[e]), c1, v[e]);
                     }
-                    if (c + 32 == D) {
+                    if (c + 1 == D / 16) {
                         dev::tc_fence_before();
                         dev::mbar_arrive(x_free);
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 32; ++e) finite = fmaf(v[e], 0.f, finite);
+                for (int e = 0; e < 16; ++e) finite = fmaf(v[e], 0.f, finite);
                 if (mine) {
                     if (whole) {
-                        __nv_bfloat16* const bo = a.out + orow * D + c;
+                        __nv_bfloat16* const bo = a.out + orow * D + 16 * c;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
+                        for (int e = 0; e < 16; e += 8)
                             *reinterpret_cast<uint4*>(bo + e) =
                                 make_uint4(dev::pack_bf16x2(v[e], v[e + 1]), dev::pack_bf16x2(v[e + 2], v[e + 3]),
                                            dev::pack_bf16x2(v[e + 4], v[e + 5]), dev::pack_bf16x2(v[e + 6], v[e + 7]));
                     } else {
-                        float* const po = a.part_o + prow * D + c;
+                        float* const po = a.part_o + prow * D + 16 * c;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
+                        for (int e = 0; e < 16; e += 4)
                             *reinterpret_cast<float4*>(po + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
                     }
                 }
@@ -609,12 +601,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-        if (a.q_tma && row == 0 && n_q) {
-            // never leave with a copy in flight
-            volatile int never = 0;
-            dev::mbar_wait(&q_full[t], (n_q - 1) & 1, &never, a.err);
-        }
-        __syncwarp();
     } else {
         regs_dec<kRegsOthers>();
         if (warp == kKWarp || warp == kVWarp) {
@@ -635,8 +621,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return blk * kBlockSize < w.it.tok1 ? __ldg(a.bt + (int64_t)w.it.req * a.max_blocks + blk) * kBlockSize
                                                     : a.num_blocks * kBlockSize;
             };
-            uint32_t g = 0;
+            uint32_t g = 0, n_q0 = 0, n_q1 = 0;      // stages, and query tiles, loaded so far
             bool ok = true;
+            // The queries of an item go ahead of its first V: the products that read the last
+            // ones are done before the slot of that V is free.
+            auto load_q = [&](const Work& w) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t& n = b ? n_q1 : n_q0;
+                    if (!ok || (b ? w.dual : w.ns0 == 0)) continue;
+                    if (n && !dev::mbar_wait(&q_free[b], (n - 1) & 1, abort_flag, a.err)) {
+                        ok = false;
+                        continue;
+                    }
+                    ++n;
+                    // (rows behind the request's are other requests' queries: computed like
+                    // the others and left alone)
+                    dev::mbar_arrive_expect_tx(&q_full[b], L::kTileQ);
+                    for (int hf = 0; hf < L::kHalves; ++hf)
+                        dev::tma_load_3d(smem + L::kOffQ + b * L::kTileQ + hf * (128 * 128), &tmQ, &q_full[b], hf * 64,
+                                         w.it.head * a.G, w.it.q0 + over_g(a, b * 128));
+                }
+            };
             Work nw = load_work(a, first);
             int32_t nxt = fetch(nw, 0);
             for (int32_t i = first; ok && i < last; ++i) {
@@ -647,6 +653,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     nxt = fetch(nw, 0);             // the next item's first batch, while this one streams
                 }
                 int32_t more = w.ns > kStagesPerBatch ? fetch(w, 1) : 0;
+                if (!is_k && a.q_tma && w.ns && lane == 0) load_q(w);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
                 for (int32_t j = 0; j < w.ns; ++j, ++g) {
                     if (j && j % kStagesPerBatch == 0) {
                         cur = more;
@@ -677,6 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 volatile int never = 0;
                 for (uint32_t j = g; j > 0 && j + NS > g; --j)
                     dev::mbar_wait(&full[(j - 1) % NS], ((j - 1) / NS) & 1, &never, a.err);
+                if (n_q0) dev::mbar_wait(&q_full[0], (n_q0 - 1) & 1, &never, a.err);
+                if (n_q1) dev::mbar_wait(&q_full[1], (n_q1 - 1) & 1, &never, a.err);
             }
         } else {
             // -------------------------------------------- MMA issue
@@ -708,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int t = 0; t < 2; ++t) {
                             if (w.dual ? (j & 1) != t : (t == 0 && j >= w.ns0)) continue;
                             const int b = w.dual ? 0 : t;
+                            const int32_t ns_t = w.dual ? w.ns : (t ? w.ns1 : w.ns0);
                             if (j == 0) wait(&q_full[b], ((b ? loads1 : loads0) - 1) & 1);
                             if (n) wait(s_free, (n - 1) & 1);
                             if (!ok) break;
@@ -720,7 +732,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     dev::tc_mma_ss(tmem + L::kColS, ad0 + off, bd0 + off, idesc, k > 0 ? 1u : 0u);
                                 }
                                 dev::tc_commit(&s_full[t]);
-                                const int32_t ns_t = w.dual ? w.ns : (t ? w.ns1 : w.ns0);
                                 if (j + 1 == ns_t) dev::tc_commit(&q_free[b]);
                             }
                             __syncwarp();
@@ -743,6 +754,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int32_t j = 0; ok && j < w.ns; ++j) {
                         const uint32_t G = g + j, s = G % L::kVSlots;
                         wait(&v_full[s], (G / L::kVSlots) & 1);
+                        if (ok && j + 1 == w.ns && w.it.tok1 % kBlockSize) {
+                            // The last block's slots behind the range were loaded too and may
+                            // hold anything, NaN included: their weights are 0, but 0 x NaN is
+                            // not, so V's rows there are cleared.
+                            const int r0 = w.it.tok1 - w.it.tok0 - j * kStage, r1 = (r0 + kBlockSize - 1) / kBlockSize * kBlockSize;
+                            uint8_t* vs = smem + L::kOffV + s * L::kKV;
+                            for (int e = lane; e < (r1 - r0) * 8 * L::kHalves; e += 32) {
+                                const int rr = r0 + e / (8 * L::kHalves), c = e % (8 * L::kHalves);
+                                *reinterpret_cast<uint4*>(vs + sw128_off(rr, c >> 3, c & 7)) = make_uint4(0, 0, 0, 0);
+                            }
+                            dev::fence_proxy_async_smem();
+                            __syncwarp();
+                        }
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             if (w.dual ? (j & 1) != t : (t == 0 && j >= w.ns0)) continue;

@@ -12,6 +12,12 @@ o = sum_j w_j v_j over the visible tokens and A = sum_j w_j |v_j|:
   sum of n terms by n 2^-24: (2 B + 2^-19 + n 2^-23) A, small beside the above;
 * the final rounding: 2^-8 |o| plus 2^-8 of all of the above.
 
+Over a row's D elements the roundings of the weights, each at most 2^-8 and
+taken as uniform and independent, add up to a vector of expected square
+2^-16 / 3 sum_j w_j^2 |v_j|^2; a row may be off by six times the root of that
+(and the terms above), which is far less than A for a row that averages many
+tokens, and so shows a token that is wrong among thousands.
+
 lse (fp32): B + 2^-20 + n 2^-24, plus 2^-23 |lse| for its own arithmetic.
 """
 import math
@@ -90,7 +96,7 @@ class Batch:
 
 
 def reference(b, r, full):
-    """(o, A, lse, B) of request r in 64 bits: [n, hq, d], [n, hq, d], [n, hq], [n, hq]."""
+    """(o, A, lse, B, N) of request r in 64 bits: [n, hq, d], [n, hq, d], and [n, hq] each."""
     torch = _torch()
     n, l, g = b.new_h[r], b.seq_h[r], b.hq // b.hkv
     s0 = b.starts_h[r]
@@ -98,7 +104,7 @@ def reference(b, r, full):
     k, v = (c.view(-1, b.hkv, b.d)[b.slot[r]].double() for c in (b.k, b.v))
     o = torch.zeros(n, b.hkv, g, b.d, dtype=torch.float64, device="cuda")
     a, lse = torch.zeros_like(o), torch.full((n, b.hkv, g), -math.inf, dtype=torch.float64, device="cuda")
-    top = torch.zeros_like(lse)
+    top, norm = torch.zeros_like(lse), torch.zeros_like(lse)
     pos = torch.arange(n, device="cuda") + (l - n)
     sees = torch.ones(n, l, dtype=torch.bool, device="cuda") if full else \
         torch.arange(l, device="cuda")[None] <= pos[:, None]
@@ -118,10 +124,11 @@ def reference(b, r, full):
         else:
             o[:, h] = torch.einsum("ngl,ld->ngd", w, vf)
         a[:, h] = torch.einsum("ngl,ld->ngd", w, vf.abs())
+        norm[:, h] = torch.einsum("ngl,l->ng", w * w, (vf * vf).sum(-1)).sqrt()
         big = torch.einsum("ngd,ld->ngl", q[:, h].abs(), k[:, h].abs()).masked_fill(~sees[:, None], 0.0)
         top[:, h] = big.amax(-1) * b.scale
     shape = (n, b.hq, b.d)
-    return o.view(shape), a.view(shape), lse.view(n, b.hq), top.view(n, b.hq) * b.d * 2.0 ** -23
+    return o.view(shape), a.view(shape), lse.view(n, b.hq), top.view(n, b.hq) * b.d * 2.0 ** -23, norm.view(n, b.hq)
 
 
 def check(b, full=False, lse=True, what=""):
@@ -130,7 +137,7 @@ def check(b, full=False, lse=True, what=""):
         if n == 0:
             continue
         s0 = b.starts_h[r]
-        o, a, ref, err = reference(b, r, full)
+        o, a, ref, err, norm = reference(b, r, full)
         got = b.out[s0:s0 + n].double()
         tol = (2 * 2.0 ** -8 + 2 * err[..., None] + 2.0 ** -19 + l * 2.0 ** -23) * a
         tol = tol + 2.0 ** -8 * (o.abs() + tol) + 1e-30
@@ -138,6 +145,10 @@ def check(b, full=False, lse=True, what=""):
         assert bool((~torch.isfinite(got) == nan).all()), f"{what}: request {r}: finite elsewhere than it should be"
         off = ((got - o).abs() / tol).masked_fill(nan, 0)
         assert bool((off <= 1).all()), f"{what}: request {r} (n {n}, L {l}): {off.max().item():.3f} of the tolerance"
+        rest = (2 * err + 2.0 ** -19 + l * 2.0 ** -23) * a.norm(dim=-1) + 2.0 ** -8 * o.masked_fill(nan, 0).norm(dim=-1)
+        tol = 6 * 2.0 ** -8 / math.sqrt(3) * norm * (1 + 2.0 ** -8) + rest + 1e-30
+        off = (got - o).masked_fill(nan, 0).norm(dim=-1) / tol
+        assert bool((off <= 1).all()), f"{what}: request {r} (n {n}, L {l}): a row is {off.max().item():.3f} of its tolerance"
         if lse:
             have = b.lse[s0:s0 + n].double()
             none = torch.isinf(ref)
@@ -220,6 +231,38 @@ def test_long_rows_are_cut_and_joined(d):
     check(b, what="cut prompts")
 
 
+@pytest.mark.parametrize("hq,hkv,d,full", [(64, 8, 64, False), (32, 8, 128, False), (16, 16, 64, True), (12, 4, 128, False)])
+def test_many_items_a_cta(hq, hkv, d, full):
+    # hundreds of short requests: every CTA walks a long list of short items, whole
+    # tiles, half tiles and single rows mixed, again and again
+    import random
+    import shared_prefix_kv_fca_b200 as fca
+    rng = random.Random(d + hq)
+    new = [rng.choice([1, 2, 17, 18, 33, 56, 70]) for _ in range(300)]
+    seq = [rng.choice([0, 1, 40, 130, 300]) if full else n + rng.choice([0, 9, 18, 120, 250]) for n in new]
+    b = Batch(seq, new, hq, hkv, d, seed=d)
+    with b.plan(full=full) as plan:
+        for _ in range(20):
+            b.attend(plan)
+        assert fca.fca_chunk_check_status(plan) == 0
+    check(b, full=full, what="many items")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_rows_over_long_caches(d):
+    # items of many stages, one after the other, whose last block is only partly filled: the
+    # slots behind it are cleared while other stages are under way
+    import random
+    rng = random.Random(d)
+    new = [rng.randint(2, 8) for _ in range(50)]
+    b = Batch([n + rng.randint(1984, 3969) for n in new], new, 16, 16, d, seed=d)
+    with b.plan() as plan:
+        for _ in range(3):
+            b.out.fill_(7.25)
+            b.attend(plan)
+            check(b, what="few rows, long caches")
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_scores_far_apart(d):
     # maxima that jump by thousands in the log domain from one stage to the
@@ -260,7 +303,7 @@ def test_what_a_row_does_not_see_has_no_part_in_it():
         k[s[325], 1, :] = 0
         ref = Batch([333, 40], [40, 40], 4, 2, d, seed=6)
         ref.k, ref.v, ref.out, ref.lse = b.k, b.v, b.out, b.lse
-        o_ref, a, _, err = reference(ref, 0, False)
+        o_ref, a, _, err, _ = reference(ref, 0, False)
         off = ((b.out[:40].double() - o_ref).abs() / ((2 ** -7 + 2 * err[..., None] + 2 ** -12) * a + 2 ** -8 * o_ref.abs()))
         early = torch.arange(40, device="cuda") < 17
         assert bool((off[early] <= 1).all())
