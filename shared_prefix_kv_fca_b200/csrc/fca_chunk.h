@@ -12,7 +12,12 @@ namespace fca {
 
 constexpr int kChunkRows = 256;      // stacked query rows a tile: two MMA tiles of 128
 constexpr int kChunkStage = 128;     // tokens a pipeline stage
-constexpr int kChunkTileCost = 1;    // a tile's own cost (query load, pipeline fill, epilogue), in stages
+// What a stage and a tile itself (query load, pipeline fill, last P V, storing) cost, in
+// units of about 0.25 us: tiles above 128 rows are bound by the softmax and the products, the
+// others by the cache's bytes.  A chunk of 1999 tokens (64/8/128) beside 95 decodes takes
+// 555 us with equal costs for all stages, 526 us at 4 : 3, 515 us at 8 : 5 and 580 us at 2 : 1.
+constexpr int kChunkStageCost = 8, kChunkTileCost = 14;
+constexpr int kChunkHalfStageCost = 5, kChunkHalfTileCost = 10;
 constexpr int kChunkMinPiece = 2;    // fewest stages a tile is cut into
 constexpr int kChunkMaxCtas = 256;
 
@@ -35,7 +40,7 @@ struct ChunkCut {
 };
 
 struct ChunkHeader {
-    int64_t work;       // total cost, in stages
+    int64_t work;       // total cost
     int64_t quota;      // cost a CTA gets
     int32_t status;     // error bits of the last build
     int32_t n_tiles;

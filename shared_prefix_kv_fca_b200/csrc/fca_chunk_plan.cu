@@ -4,7 +4,7 @@
 // The rows of a request that read one KV head -- n tokens x G query heads -- are
 // stacked and cut into tiles of 256.  Tile i of a request with L cached tokens
 // sees the first l_i = L - n + ceil(256 (i + 1) / G) of them (the last tile L),
-// that is ceil(l_i / 128) stages, and costs that many plus kChunkTileCost.  All tiles
+// that is ceil(l_i / 128) stages, and costs so much for each stage and for itself.  All tiles
 // of the step, in the order (request, KV head, tile), form one line of
 // cost W; CTA c gets the stretch [c Q, (c + 1) Q), Q = W / CTAs.  So every CTA has the
 // same work to within a stage, whatever the mix of long and short requests, and
@@ -80,11 +80,24 @@ __device__ __forceinline__ int32_t stages_for(int64_t tokens) {
     return (int32_t)((tokens + kChunkStage - 1) / kChunkStage);
 }
 
-// Cost of a request's tiles [0, i) of one KV head, i below its tile count.
+// Cost of a request's tiles [0, i) of one KV head, i below its tile count (so that all are full).
 __device__ int64_t cost_before(int32_t i, int32_t n, int32_t L, int32_t G, bool whole) {
-    if (whole) return (int64_t)i * (stages_for(L) + kChunkTileCost);
     const int64_t m = (int64_t)kChunkStage * G;
-    return floor_sum(i, m, kChunkRows, (int64_t)(L - n) * G + kChunkRows + m - 1) + (int64_t)i * kChunkTileCost;
+    const int64_t stages = whole ? (int64_t)i * stages_for(L)
+                                 : floor_sum(i, m, kChunkRows, (int64_t)(L - n) * G + kChunkRows + m - 1);
+    return stages * kChunkStageCost + (int64_t)i * kChunkTileCost;
+}
+
+// Cost of a tile of `rows` rows and ns stages.
+__device__ __forceinline__ int64_t tile_cost(int64_t rows, int32_t ns) {
+    return rows > kChunkRows / 2 ? (int64_t)ns * kChunkStageCost + kChunkTileCost
+                                 : (int64_t)ns * kChunkHalfStageCost + kChunkHalfTileCost;
+}
+
+// Cost of all of a request's tiles of one KV head.
+__device__ __forceinline__ int64_t head_cost(int32_t n, int32_t L, int32_t G, bool whole) {
+    const int32_t nt = tiles_of(n, G);
+    return cost_before(nt - 1, n, L, G, whole) + tile_cost((int64_t)n * G - (int64_t)(nt - 1) * kChunkRows, stages_for(L));
 }
 
 // Lengths checked and copied; tiles and cost before each request; the CTA's
@@ -117,9 +130,8 @@ __global__ void __launch_bounds__(kScanThreads) k_chunk_scan(ChunkPlanArgs a) {
         a.qs[r] = refused ? 0 : q0;
         a.bad[r] = 0;
         if (n > 0) {
-            const int32_t nt = tiles_of(n, a.G);
-            tiles += (int64_t)nt * a.Hkv;
-            cost += a.Hkv * (cost_before(nt - 1, n, L, a.G, a.full || L == 0) + stages_for(L) + kChunkTileCost);
+            tiles += (int64_t)tiles_of(n, a.G) * a.Hkv;
+            cost += a.Hkv * head_cost(n, L, a.G, a.full || L == 0);
         }
     }
     if (bits) atomicOr(&status, bits);
@@ -152,12 +164,11 @@ __global__ void __launch_bounds__(kScanThreads) k_chunk_scan(ChunkPlanArgs a) {
         a.cost_off[r] = at_c;
         const int32_t n = refused ? 0 : a.qs_in[r + 1] - a.qs_in[r], L = a.seq[r];
         if (n > 0) {
-            const int32_t nt = tiles_of(n, a.G);
-            at_t += (int64_t)nt * a.Hkv;
-            at_c += a.Hkv * (cost_before(nt - 1, n, L, a.G, a.full || L == 0) + stages_for(L) + kChunkTileCost);
+            at_t += (int64_t)tiles_of(n, a.G) * a.Hkv;
+            at_c += a.Hkv * head_cost(n, L, a.G, a.full || L == 0);
         }
     }
-    const int64_t quota = max((W + a.ctas - 1) / a.ctas, (int64_t)(2 * kChunkMinPiece + kChunkTileCost));
+    const int64_t quota = max((W + a.ctas - 1) / a.ctas, (int64_t)(2 * kChunkMinPiece * kChunkHalfStageCost + kChunkHalfTileCost));
     const int32_t used = (int32_t)((W + quota - 1) / quota);
     if (tid < a.ctas) {
         a.cuts[tid].nrows = 0;
@@ -222,12 +233,13 @@ __global__ void __launch_bounds__(kListThreads) k_chunk_lists(ChunkPlanArgs a) {
     const int32_t r = lo, q0 = a.qs[r], n = a.qs[r + 1] - q0, L = a.seq[r], G = a.G;
     const bool whole = a.full || L == 0;    // every row sees all L
     const int32_t nt = tiles_of(n, G), head = (t - a.tile_off[r]) / nt, i = (t - a.tile_off[r]) % nt;
-    const int64_t per_head = cost_before(nt - 1, n, L, G, whole) + stages_for(L) + kChunkTileCost;
-    const int64_t s = a.cost_off[r] + head * per_head + cost_before(i, n, L, G, whole);
+    const int64_t s = a.cost_off[r] + head * head_cost(n, L, G, whole) + cost_before(i, n, L, G, whole);
     const int64_t row0 = (int64_t)i * kChunkRows, row1 = min(row0 + kChunkRows, (int64_t)n * G);
     const int32_t seen = whole ? L : (int32_t)((L - n) + (row1 + G - 1) / G);
     const int32_t ns = stages_for(seen);
-    const int64_t e = s + ns + kChunkTileCost;
+    const int64_t e = s + tile_cost(row1 - row0, ns);
+    const bool half = row1 - row0 <= kChunkRows / 2;
+    const int64_t own = half ? kChunkHalfTileCost : kChunkTileCost, per_stage = half ? kChunkHalfStageCost : kChunkStageCost;
 
     ChunkItem it;
     it.req = r;
@@ -243,7 +255,7 @@ __global__ void __launch_bounds__(kListThreads) k_chunk_lists(ChunkPlanArgs a) {
     int32_t owner = s == 0 ? 0 : (int32_t)((s + Q - 1) / Q) - 1;
     int32_t k = 0, first_cut = 0, last_cut = 0;
     for (int32_t c = max(1, (int32_t)((s + Q - 1) / Q)); c < used && (int64_t)c * Q < e; ++c) {
-        const int64_t x = (int64_t)c * Q - s - kChunkTileCost;      // the boundary's stage
+        const int64_t x = max((int64_t)0, (int64_t)c * Q - s - own) / per_stage;     // the boundary's stage
         int32_t next = t, prev_end = t;                             // tiles on the two sides
         if (x < kChunkMinPiece) {
             prev_end = t - 1;
