@@ -406,7 +406,7 @@ fca_status fca_paged_decode_static(const void *q, const void *k_cache, const voi
  * do), FCA_ERR_UNSUPPORTED (over 16384 requests, or
  * num_blocks or max_blocks beyond 2^31 / 16), FCA_ERR_CUDA.  num_requests == 0
  * sets q_starts[0] to 0, the slots to -1 and free_after.  Asynchronous on
- * `stream`, one kernel, no workspace; runs on the current device.
+ * `stream`, one kernel or two, no workspace; runs on the current device.
  */
 fca_status fca_extend_tables(int32_t *block_tables, int32_t max_blocks, const int32_t *cached_lens,
                              const int32_t *new_lens, int32_t num_requests, const int32_t *free_blocks,

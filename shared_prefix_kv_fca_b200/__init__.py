@@ -165,6 +165,8 @@ def _stream_handle(stream, device: Optional[int] = None) -> Optional[int]:
     `device` (of the current device when that is None too)."""
     if stream is None:
         import torch
+        if device is not None:      # the handle alone, without a Stream object around it
+            return torch._C._cuda_getCurrentRawStream(device)
         stream = torch.cuda.current_stream(device)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -193,9 +195,14 @@ def _on_device(idx: Optional[int]):
     """Context that makes CUDA device `idx` current for the call (no change
     when no tensor named a device)."""
     if idx is None:
-        return contextlib.nullcontext()
+        return _NO_CHANGE
     import torch
+    if torch.cuda.is_initialized() and torch.cuda.current_device() == idx:
+        return _NO_CHANGE
     return torch.cuda.device(idx)
+
+
+_NO_CHANGE = contextlib.nullcontext()
 
 
 def _check_tables(block_tables, seq_lens) -> None:
@@ -207,9 +214,10 @@ def _check_tables(block_tables, seq_lens) -> None:
 
 
 def _check_bf16(t, name: str, shape=None) -> None:
-    if not t.is_cuda or str(t.dtype) != "torch.bfloat16" or not t.is_contiguous():
+    import torch
+    if t.dtype is not torch.bfloat16 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous bf16 CUDA tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
@@ -217,7 +225,8 @@ def _check_caches(k_cache, v_cache, num_blocks: int, Hkv: int, D: int) -> None:
     """The kernels read num_blocks x 16 x Hkv x D elements of each cache."""
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         _check_bf16(t, name)
-        if t.dim() != 4 or tuple(t.shape[1:]) != (16, Hkv, D) or t.shape[0] < num_blocks:
+        shape = t.shape
+        if len(shape) != 4 or shape[1:] != (16, Hkv, D) or shape[0] < num_blocks:
             raise ValueError(f"{name} must be [>= {num_blocks}, 16, {Hkv}, {D}], not {tuple(t.shape)}")
 
 
@@ -352,20 +361,22 @@ def fca_paged_decode_static(q, k_cache, v_cache, block_tables, seq_lens, num_blo
 
 
 def _check_ints(t, name: str, shape=None, least: int = 0) -> None:
-    if not t.is_cuda or str(t.dtype) != "torch.int32" or not t.is_contiguous():
+    import torch
+    if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 CUDA tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.numel() < least:
+    if least and t.numel() < least:
         raise ValueError(f"{name} must have at least {least} element(s)")
 
 
 def _check_rows(t, name: str, shape) -> int:
     """A bf16 tensor [rows, heads, D] whose rows are contiguous but may be
     apart (views of a wider projection output); returns the row stride."""
-    if not t.is_cuda or str(t.dtype) != "torch.bfloat16":
+    import torch
+    if t.dtype is not torch.bfloat16 or not t.is_cuda:
         raise ValueError(f"{name} must be a bf16 CUDA tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     rows, heads, D = shape
     packed = heads * D
@@ -373,11 +384,12 @@ def _check_rows(t, name: str, shape) -> int:
         if not t.is_contiguous():
             raise ValueError(f"{name}: each row of {heads} heads must be contiguous")
         return packed
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+    row, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != D):
         raise ValueError(f"{name}: each row of {heads} heads must be contiguous")
-    if t.stride(0) < packed or t.stride(0) % 8:
-        raise ValueError(f"{name}: rows must be a multiple of 8 elements apart, at least {packed}, not {t.stride(0)}")
-    return int(t.stride(0))
+    if row < packed or row % 8:
+        raise ValueError(f"{name}: rows must be a multiple of 8 elements apart, at least {packed}, not {row}")
+    return row
 
 
 def fca_extend_tables(block_tables, cached_lens, new_lens, free_blocks, free_next, num_blocks: int, seq_lens,
@@ -412,10 +424,10 @@ def fca_extend_tables(block_tables, cached_lens, new_lens, free_blocks, free_nex
                       ("q_starts", q_starts), ("slots", slots), ("free_after", free_after),
                       ("dev_status", dev_status))
     with _on_device(dev):
-        rc = lib.fca_extend_tables(_ptr(block_tables), mb, _ptr(cached_lens), _ptr(new_lens), R, _ptr(free_blocks),
-                                   free_blocks.numel(), _ptr(free_next), num_blocks, _ptr(seq_lens), _ptr(q_starts),
-                                   _ptr(slots), slots.numel(), _ptr(free_after), _ptr(dev_status),
-                                   _stream_handle(stream, dev))
+        rc = lib.fca_extend_tables(block_tables.data_ptr(), mb, cached_lens.data_ptr(), new_lens.data_ptr(), R,
+                                   free_blocks.data_ptr(), free_blocks.numel(), free_next.data_ptr(), num_blocks,
+                                   seq_lens.data_ptr(), q_starts.data_ptr(), slots.data_ptr(), slots.numel(),
+                                   free_after.data_ptr(), _ptr(dev_status), _stream_handle(stream, dev))
     _check(rc, "fca_extend_tables")
 
 
@@ -436,8 +448,8 @@ def fca_append_kv(k, v, slots, k_cache, v_cache, num_blocks: int, dev_status=Non
     dev = _one_device(("k", k), ("v", v), ("slots", slots), ("k_cache", k_cache), ("v_cache", v_cache),
                       ("dev_status", dev_status))
     with _on_device(dev):
-        rc = lib.fca_append_kv(_ptr(k), ks, _ptr(v), vs, _ptr(slots), T, num_blocks, Hkv, D, _ptr(k_cache),
-                               _ptr(v_cache), _ptr(dev_status), _stream_handle(stream, dev))
+        rc = lib.fca_append_kv(k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), T, num_blocks, Hkv, D,
+                               k_cache.data_ptr(), v_cache.data_ptr(), _ptr(dev_status), _stream_handle(stream, dev))
     _check(rc, "fca_append_kv")
 
 
@@ -488,8 +500,8 @@ def fca_chunk_attention(q, k_cache, v_cache, plan: "ChunkPlan", out, lse=None, s
     _check_caches(k_cache, v_cache, plan.num_blocks, plan.num_kv_heads, plan.head_dim)
     _check_lse(lse, plan.num_tokens, plan.num_q_heads)
     _plan_device(plan, ("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("out", out), ("lse", lse))
-    _check(lib.fca_chunk_attention(_ptr(q), stride, _ptr(k_cache), _ptr(v_cache), plan.handle, _ptr(out), _ptr(lse),
-                                   float(scale), _stream_handle(stream, plan.device)), "fca_chunk_attention")
+    _check(lib.fca_chunk_attention(q.data_ptr(), stride, k_cache.data_ptr(), v_cache.data_ptr(), plan.handle,
+                                   out.data_ptr(), _ptr(lse), float(scale), _stream_handle(stream, plan.device)), "fca_chunk_attention")
 
 
 def fca_chunk_check_status(plan: "ChunkPlan", stream=None) -> int:

@@ -10,27 +10,25 @@
 // block's first position is a multiple of 16 that is a new token's, so the
 // thread with that token also writes the table entry: one pass over tokens.
 //
-// The work is a few hundred kilobytes at most and bound by latency: one
-// launch, no workspace.  One cluster of CTAs (one CTA for small steps); each CTA
-// sums all the lengths itself into its shared memory (reading 2 R integers
-// again costs less than passing sums around), the tokens are dealt out over the
-// cluster.  Every thread first finds and checks its slots, the CTAs exchange
-// the verdict through distributed shared memory, and behind that cluster
-// barrier either everything is written or nothing: every input has been read by
-// then, so lengths and list position may be updated in place.
+// The work is a megabyte or two at most and bound by latency and, with many
+// tokens, by the instructions of the lookups.  Every CTA sums all the lengths and checks
+// all the ids that would be used itself (a few tens of kilobytes from L2), so that
+// each comes to the same verdict -- everything is written or nothing -- without an exchange.
+// The tokens are dealt out over the warps of all CTAs.  Small steps are one CTA and
+// one launch; there, lengths and list position are written behind a barrier, all
+// CTA's reads done, and may be updated in place.  Large ones leave those two to a second
+// launch of one CTA (2048 prompts, 262144 tokens: 129 us with the tokens' slots found
+// by a search each on a cluster of 8 CTAs, 47 us with the lookup below, and 10.8 us over
+// 148 CTAs; a decode step of 256 requests takes 6.0 us).
 #include <algorithm>
-#include <cooperative_groups.h>
 
 #include "fca_internal.h"
 
 namespace fca {
 namespace {
 
-namespace cg = cooperative_groups;
-
 constexpr int kThreads = 1024;
-constexpr int kCluster = 8;     // CTAs for large steps (the largest portable cluster)
-constexpr int kKeep = 4;        // slots a thread keeps in registers between check and write
+constexpr int kWide = 4;        // tokens a lane has under way at once
 
 struct TablesArgs {
     int32_t* bt;
@@ -44,6 +42,7 @@ struct TablesArgs {
     int32_t* free_after;
     int32_t* err;
     int32_t R, max_blocks, num_free, num_blocks, num_slots;
+    int32_t lengths;             // whether this launch writes seq_lens and free_after
 };
 
 // Exclusive sum over the CTA's threads of two 64-bit values; totals in ta, tb.
@@ -98,10 +97,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend_tables(TablesArgs a) {
     int32_t* const first = sm + a.R + 1;          // [R] place of the request's first new block on the list
     int32_t* const had = first + a.R;             // [R] cached tokens
     __shared__ int64_t part[kThreads / 32][2];
-    __shared__ int32_t verdict[kCluster];
     __shared__ int32_t bits;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int rank = blockIdx.x, ranks = gridDim.x;
     const int tid = threadIdx.x, lane = tid & 31;
     const int32_t R = a.R;
     if (tid == 0) bits = 0;      // (the scan's barrier lies between this and the first use)
@@ -140,72 +137,93 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend_tables(TablesArgs a) {
     __syncthreads();
     bad = bits;
 
-    // Request, position and block id of token t (left alone behind the last one).
-    // The searches for the warp's first and last token bound each lane's own.
+    // the ids that would be used: the list's, and the last blocks that get more tokens
     const int32_t total = (int32_t)all_tok;
-    auto slot_of = [&](int32_t t, int32_t& row, int32_t& col, int32_t& id) {
-        const int32_t t0 = t - lane;
-        const int32_t lo = find_request(start, min(t0, total - 1), 0, R - 1);
-        const int32_t hi = find_request(start, min(t0 + 31, total - 1), lo, R - 1);
-        if (t >= total) return;
-        const int32_t r = find_request(start, t, lo, hi);
-        const int32_t c = had[r], p = c + (t - start[r]), j = p / kBlockSize, h = (c + kBlockSize - 1) / kBlockSize;
-        id = j < h ? a.bt[(int64_t)r * a.max_blocks + j] : a.free_blocks[first[r] + j - h];
-        row = r;
-        col = p;
-    };
-    const int32_t stride = ranks * kThreads, t_first = rank * kThreads + tid;
-    int32_t k_row[kKeep], k_col[kKeep], k_id[kKeep];
+    const int32_t stride = ranks * kThreads, mine = rank * kThreads + tid;
     if (!bad) {
-#pragma unroll
-        for (int i = 0; i < kKeep; ++i) {
-            k_row[i] = -1;
-            const int64_t t = t_first + (int64_t)i * stride;
-            if (t - lane < total) {
-                slot_of((int32_t)t, k_row[i], k_col[i], k_id[i]);
-                if (k_row[i] >= 0 && (k_id[i] < 0 || k_id[i] >= a.num_blocks)) bad |= kErrStaticBlockId;
-            }
+        for (int64_t x = tid; x < all_blk; x += kThreads) {
+            const int32_t id = a.free_blocks[next + x];
+            if (id < 0 || id >= a.num_blocks) bad = kErrStaticBlockId;
         }
-        for (int64_t t = t_first + (int64_t)kKeep * stride; t - lane < total; t += stride) {
-            int32_t row = -1, col = 0, id = 0;
-            slot_of((int32_t)t, row, col, id);
-            if (row >= 0 && (id < 0 || id >= a.num_blocks)) bad |= kErrStaticBlockId;
+        for (int32_t r = tid; r < R; r += kThreads) {
+            if (had[r] % kBlockSize == 0 || start[r + 1] == start[r]) continue;
+            const int32_t id = a.bt[(int64_t)r * a.max_blocks + had[r] / kBlockSize];
+            if (id < 0 || id >= a.num_blocks) bad = kErrStaticBlockId;
         }
     }
     __syncthreads();             // (everyone has read `bits`)
     if (bad) atomicOr(&bits, bad);
     __syncthreads();
-    if (tid < ranks) *cluster.map_shared_rank(&verdict[rank], tid) = bits;
-    cluster.sync();
-    bad = 0;
-    for (int i = 0; i < ranks; ++i) bad |= verdict[i];
+    bad = bits;
 
-    for (int32_t r = rank * kThreads + tid; r <= R; r += stride) {
+    for (int32_t r = mine; r <= R; r += stride) {
         a.q_starts[r] = bad ? 0 : start[r];
-        if (r < R) a.seq_lens[r] = bad ? had[r] : had[r] + start[r + 1] - start[r];
+        if (a.lengths && r < R) a.seq_lens[r] = bad ? had[r] : had[r] + start[r + 1] - start[r];
     }
     if (rank == 0 && tid == 0) {
-        *a.free_after = bad ? next : next + (int32_t)all_blk;
+        if (a.lengths) *a.free_after = bad ? next : next + (int32_t)all_blk;
         if (bad && a.err) atomicOr(a.err, bad);
     }
     if (bad) {
-        for (int64_t t = t_first; t < a.num_slots; t += stride) a.slots[t] = -1;
+        for (int64_t t = mine; t < a.num_slots; t += stride) a.slots[t] = -1;
         return;
     }
-    auto put = [&](int32_t t, int32_t row, int32_t col, int32_t id) {
-        a.slots[t] = row < 0 ? -1 : id * kBlockSize + col % kBlockSize;
-        if (row >= 0 && col % kBlockSize == 0) a.bt[(int64_t)row * a.max_blocks + col / kBlockSize] = id;
-    };
+    // Each warp takes a stretch of the slots, kWide tokens a lane at a time.  The request
+    // of a window of 32 tokens is found by stepping over the next 32 starts at once: a
+    // search from scratch per token costs twenty times the instructions.
+    const int32_t windows = (a.num_slots + 31) / 32, warps = stride / 32, warp = mine / 32;
+    const int32_t w0 = (int32_t)((int64_t)windows * warp / warps), w1 = (int32_t)((int64_t)windows * (warp + 1) / warps);
+    int32_t r_cur = w0 < w1 && w0 * 32 < total ? find_request(start, w0 * 32, 0, R - 1) : 0;
+    for (int32_t w = w0; w < w1; w += kWide) {
+        int32_t row[kWide], pos[kWide], id[kWide];
 #pragma unroll
-    for (int i = 0; i < kKeep; ++i) {
-        const int64_t t = t_first + (int64_t)i * stride;
-        if (t < a.num_slots) put((int32_t)t, k_row[i], k_col[i], k_id[i]);
+        for (int i = 0; i < kWide; ++i) {
+            const int32_t t0 = (w + i) * 32, t = t0 + lane;
+            row[i] = -1;
+            if (w + i >= w1 || t0 >= total) continue;
+            const int32_t t_last = min(t0 + 31, total - 1);
+            int32_t next_start, n;
+            do {                                   // the request that holds t0
+                next_start = start[min(R, r_cur + 1 + lane)];
+                n = __popc(__ballot_sync(0xffffffffu, r_cur + 1 + lane < R && next_start <= t0));
+                r_cur += n;
+            } while (n == 32);
+            if (n) next_start = start[min(R, r_cur + 1 + lane)];
+            int32_t r = r_cur;
+            n = __popc(__ballot_sync(0xffffffffu, r_cur + 1 + lane < R && next_start <= t_last));
+            if (n == 32)                           // (many requests without tokens)
+                r = find_request(start, min(t, t_last), r_cur, R - 1);
+            else
+                for (int k = 0; k < n; ++k) r += t >= __shfl_sync(0xffffffffu, next_start, k);
+            if (t >= total) continue;
+            const int32_t c = had[r], p = c + (t - start[r]), j = p / kBlockSize, h = (c + kBlockSize - 1) / kBlockSize;
+            row[i] = r;
+            pos[i] = p;
+            id[i] = j < h ? a.bt[(int64_t)r * a.max_blocks + j] : a.free_blocks[first[r] + j - h];
+        }
+#pragma unroll
+        for (int i = 0; i < kWide; ++i) {
+            const int64_t t = (int64_t)(w + i) * 32 + lane;
+            if (w + i >= w1 || t >= a.num_slots) continue;
+            a.slots[t] = row[i] < 0 ? -1 : id[i] * kBlockSize + pos[i] % kBlockSize;
+            // a block's first position is new exactly when the block is
+            if (row[i] >= 0 && pos[i] % kBlockSize == 0) a.bt[(int64_t)row[i] * a.max_blocks + pos[i] / kBlockSize] = id[i];
+        }
     }
-    for (int64_t t = t_first + (int64_t)kKeep * stride; t - lane < a.num_slots; t += stride) {
-        int32_t row = -1, col = 0, id = 0;
-        if (t - lane < total) slot_of((int32_t)t, row, col, id);
-        if (t < a.num_slots) put((int32_t)t, row, col, id);
+}
+
+// The lengths and the list position of a large step, from the rows that it was given.
+__global__ void __launch_bounds__(kThreads, 1) k_extend_lengths(TablesArgs a) {
+    __shared__ int64_t part[kThreads / 32][2];
+    int64_t blocks = 0;
+    for (int32_t r = threadIdx.x; r < a.R; r += kThreads) {
+        const int32_t c = a.cached[r], n = a.q_starts[r + 1] - a.q_starts[r];
+        if (n > 0) blocks += (c + n + kBlockSize - 1) / kBlockSize - (c + kBlockSize - 1) / kBlockSize;
+        a.seq_lens[r] = c + n;
     }
+    int64_t x, y, all, none;
+    block_scan2(blocks, 0, part, x, y, all, none);
+    if (threadIdx.x == 0) *a.free_after = *a.free_next + (int32_t)all;
 }
 
 bool overlap(const void* p, size_t np, const void* q, size_t nq) {
@@ -261,23 +279,15 @@ extern "C" fca_status fca_extend_tables(int32_t* block_tables, int32_t max_block
         (void)cudaGetLastError();
         return FCA_ERR_CUDA;
     }
-    // One CTA while its threads hold every slot between check and write.
-    const int ctas = num_slots <= kKeep * kThreads ? 1 : kCluster;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (note_cuda(cudaLaunchKernelEx(&cfg, k_extend_tables, a)) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return FCA_ERR_CUDA;
-    }
+    // One CTA while a warp has one round of slots at most (a second launch costs as much as two or
+    // three rounds: 19000 slots take 33 us on one CTA, 12.9 us on 5, 8.4 us on 19); else a
+    // window a warp, up to one CTA per SM.
+    const int64_t want = num_slots <= kWide * kThreads ? 1 : ((int64_t)num_slots + kThreads - 1) / kThreads;
+    const int ctas = (int)std::min<int64_t>(want, 148);
+    a.lengths = ctas == 1;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    k_extend_tables<<<ctas, kThreads, smem, s>>>(a);
+    if (ctas > 1 && cudaPeekAtLastError() == cudaSuccess) k_extend_lengths<<<1, kThreads, 0, s>>>(a);
+    if (note_cuda(cudaGetLastError()) != cudaSuccess) return FCA_ERR_CUDA;
     return FCA_OK;
 }
