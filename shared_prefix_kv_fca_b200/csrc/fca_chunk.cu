@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_chunk(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
             const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmQ) {
     using L = Layout<D>;
+    dev::pdl_launch_dependents();           // the merge may be set up
     const int32_t first = a.begin[blockIdx.x], last = a.end[blockIdx.x];
     if (first >= last) return;
 
@@ -810,11 +811,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // The pieces of a cut tile joined by their weights: a warp a row.
-constexpr int kMergeThreads = 256, kMergeSplit = 4;     // CTAs a tile
+constexpr int kMergeThreads = 256, kMergeSplit = 16;     // CTAs a tile: 2 rows a warp at most
 
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) k_chunk_merge(ChunkArgs a, const ChunkCut* cuts) {
     constexpr int E = D / 32;
+    dev::pdl_wait();
     const ChunkCut cut = cuts[blockIdx.x];
     const int lane = threadIdx.x & 31, pieces = cut.cta1 - cut.cta0 + 1;
     for (int32_t row = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); row < cut.nrows;
@@ -925,12 +927,19 @@ extern "C" fca_status fca_chunk_attention(const void* q, int64_t q_row_stride, c
     const cudaError_t e = plan->D == 128 ? launch_chunk<128>(a, tk, tv, tq, plan->ctas, s) : launch_chunk<64>(a, tk, tv, tq, plan->ctas, s);
     if (note_cuda(e) != cudaSuccess) return FCA_ERR_CUDA;
     if (plan->may_cut) {
-        const dim3 grid(plan->ctas, kMergeSplit);
-        if (plan->D == 128)
-            k_chunk_merge<128><<<grid, kMergeThreads, 0, s>>>(a, plan->cuts);
-        else
-            k_chunk_merge<64><<<grid, kMergeThreads, 0, s>>>(a, plan->cuts);
-        if (note_cuda(cudaGetLastError()) != cudaSuccess) return FCA_ERR_CUDA;
+        // set up while the tiles run, which it waits for
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(plan->ctas, kMergeSplit);
+        cfg.blockDim = dim3(kMergeThreads);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (note_cuda(cudaLaunchKernelEx(&cfg, plan->D == 128 ? k_chunk_merge<128> : k_chunk_merge<64>, a,
+                                         (const ChunkCut*)plan->cuts)) != cudaSuccess)
+            return FCA_ERR_CUDA;
     }
     return FCA_OK;
 }

@@ -28,6 +28,7 @@ namespace {
 constexpr int kScanThreads = 1024;
 constexpr int kListThreads = 256;
 constexpr int kSegment = 1024;      // table entries a copy unit
+constexpr int kListShared = 4096;   // requests whose offsets the list kernel keeps in shared memory
 
 struct ChunkPlanArgs {
     const int32_t* bt_in;
@@ -49,27 +50,34 @@ struct ChunkPlanArgs {
     int32_t* status;
 };
 
-// sum over i in [0, n) of floor((a i + b) / m); a, b, n >= 0, m >= 1.
-__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+// sum over i in [0, n) of floor((a i + b) / m); a, b, n >= 0, m >= 1; T holds a n + b.
+template <typename T>
+__device__ int64_t floor_sum_in(T n, T m, T a, T b) {
     int64_t s = 0;
     while (n > 0) {
         if (a >= m) {
-            s += (n - 1) * n / 2 * (a / m);
+            s += (int64_t)(n - 1) * n / 2 * (a / m);
             a %= m;
         }
         if (b >= m) {
-            s += n * (b / m);
+            s += (int64_t)n * (b / m);
             b %= m;
         }
-        const int64_t y = a * n + b;
+        const T y = a * n + b;
         if (y < m) break;
         n = y / m;
         b = y % m;
-        const int64_t t = m;
+        const T t = m;
         m = a;
         a = t;
     }
     return s;
+}
+
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+    // (a 64-bit division takes five times a 32-bit one, and the sums are on the way of every launch)
+    if (a * n + b < INT32_MAX) return floor_sum_in<uint32_t>((uint32_t)n, (uint32_t)m, (uint32_t)a, (uint32_t)b);
+    return floor_sum_in<int64_t>(n, m, a, b);
 }
 
 __device__ __forceinline__ int32_t tiles_of(int32_t n, int32_t G) {
@@ -105,6 +113,7 @@ __device__ __forceinline__ int64_t head_cost(int32_t n, int32_t L, int32_t G, bo
 __global__ void __launch_bounds__(kScanThreads) k_chunk_scan(ChunkPlanArgs a) {
     __shared__ int64_t part[32][2];
     __shared__ int32_t status;
+    dev::pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t R = a.R, per = (R + kScanThreads - 1) / kScanThreads;
     const int32_t r0 = min(R, tid * per), r1 = min(R, r0 + per);
@@ -118,6 +127,7 @@ __global__ void __launch_bounds__(kScanThreads) k_chunk_scan(ChunkPlanArgs a) {
     const bool refused = __syncthreads_or(bits) != 0;
 
     int64_t tiles = 0, cost = 0;
+    int64_t head = 0;           // the last request's cost, the only one of most threads
     for (int32_t r = r0; r < r1; ++r) {
         const int32_t q0 = a.qs_in[r], n = refused ? 0 : a.qs_in[r + 1] - q0;
         int32_t L = a.seq_in[r];
@@ -131,7 +141,8 @@ __global__ void __launch_bounds__(kScanThreads) k_chunk_scan(ChunkPlanArgs a) {
         a.bad[r] = 0;
         if (n > 0) {
             tiles += (int64_t)tiles_of(n, a.G) * a.Hkv;
-            cost += a.Hkv * head_cost(n, L, a.G, a.full || L == 0);
+            head = head_cost(n, L, a.G, a.full || L == 0);
+            cost += a.Hkv * head;
         }
     }
     if (bits) atomicOr(&status, bits);
@@ -165,7 +176,7 @@ __global__ void __launch_bounds__(kScanThreads) k_chunk_scan(ChunkPlanArgs a) {
         const int32_t n = refused ? 0 : a.qs_in[r + 1] - a.qs_in[r], L = a.seq[r];
         if (n > 0) {
             at_t += (int64_t)tiles_of(n, a.G) * a.Hkv;
-            at_c += a.Hkv * head_cost(n, L, a.G, a.full || L == 0);
+            at_c += a.Hkv * (r + 1 == r1 ? head : head_cost(n, L, a.G, a.full || L == 0));
         }
     }
     const int64_t quota = max((W + a.ctas - 1) / a.ctas, (int64_t)(2 * kChunkMinPiece * kChunkHalfStageCost + kChunkHalfTileCost));
@@ -193,6 +204,7 @@ __global__ void __launch_bounds__(kScanThreads) k_chunk_scan(ChunkPlanArgs a) {
 
 // One thread places one tile; the last CTAs copy and check the tables.
 __global__ void __launch_bounds__(kListThreads) k_chunk_lists(ChunkPlanArgs a) {
+    dev::pdl_wait();
     if ((int32_t)blockIdx.x >= a.tile_ctas) {
         const int32_t segs = (a.max_blocks + kSegment - 1) / kSegment;
         const int64_t units = (int64_t)a.R * segs;
@@ -217,15 +229,23 @@ __global__ void __launch_bounds__(kListThreads) k_chunk_lists(ChunkPlanArgs a) {
         }
         return;
     }
+    __shared__ int32_t offs[kListShared];
     const int32_t N = a.hdr->n_tiles;
     const int64_t Q = a.hdr->quota;
     const int32_t used = a.hdr->n_ctas;
     const int32_t t = blockIdx.x * kListThreads + threadIdx.x;
+    if ((int32_t)blockIdx.x * kListThreads >= N) return;
+    const int32_t* off = a.tile_off;
+    if (a.R <= kListShared) {               // a search in shared memory instead of L2
+        for (int32_t r = threadIdx.x; r < a.R; r += kListThreads) offs[r] = a.tile_off[r];
+        off = offs;
+        __syncthreads();
+    }
     if (t >= N) return;
     int32_t lo = 0, hi = a.R - 1;           // the last request whose tiles begin at or before t
     while (lo < hi) {
         const int32_t mid = (lo + hi + 1) >> 1;
-        if (a.tile_off[mid] <= t)
+        if (off[mid] <= t)
             lo = mid;
         else
             hi = mid - 1;
@@ -352,8 +372,17 @@ cudaError_t build_lists(const fca_chunk_plan_s* P, const int32_t* bt, const int3
     k_chunk_scan<<<1, kScanThreads, 0, stream>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    k_chunk_lists<<<a.tile_ctas + copy_ctas, kListThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    // set up while the scan runs, which it waits for
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(a.tile_ctas + copy_ctas);
+    cfg.blockDim = dim3(kListThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_chunk_lists, a);
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
