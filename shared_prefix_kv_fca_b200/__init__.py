@@ -191,13 +191,23 @@ def _one_device(*named) -> int:
     return idx
 
 
+def _same_device(names: str, *tensors) -> int:
+    """_one_device for tensors whose names are the words of `names`, without a
+    pair for each where they agree, as they nearly always do."""
+    first = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != first:
+            return _one_device(*zip(names.split(), tensors))
+    return first.index
+
+
 def _on_device(idx: Optional[int]):
     """Context that makes CUDA device `idx` current for the call (no change
     when no tensor named a device)."""
     if idx is None:
         return _NO_CHANGE
     import torch
-    if torch.cuda.is_initialized() and torch.cuda.current_device() == idx:
+    if torch.cuda.is_initialized() and torch._C._cuda_getDevice() == idx:
         return _NO_CHANGE
     return torch.cuda.device(idx)
 
@@ -419,10 +429,9 @@ def fca_extend_tables(block_tables, cached_lens, new_lens, free_blocks, free_nex
     _check_ints(free_after, "free_after", least=1)
     if dev_status is not None:
         _check_ints(dev_status, "dev_status", least=1)
-    dev = _one_device(("block_tables", block_tables), ("cached_lens", cached_lens), ("new_lens", new_lens),
-                      ("free_blocks", free_blocks), ("free_next", free_next), ("seq_lens", seq_lens),
-                      ("q_starts", q_starts), ("slots", slots), ("free_after", free_after),
-                      ("dev_status", dev_status))
+    dev = _same_device("block_tables cached_lens new_lens free_blocks free_next seq_lens q_starts slots free_after "
+                       "dev_status", block_tables, cached_lens, new_lens, free_blocks, free_next, seq_lens, q_starts,
+                       slots, free_after, dev_status)
     with _on_device(dev):
         rc = lib.fca_extend_tables(block_tables.data_ptr(), mb, cached_lens.data_ptr(), new_lens.data_ptr(), R,
                                    free_blocks.data_ptr(), free_blocks.numel(), free_next.data_ptr(), num_blocks,
@@ -445,8 +454,7 @@ def fca_append_kv(k, v, slots, k_cache, v_cache, num_blocks: int, dev_status=Non
     _check_caches(k_cache, v_cache, num_blocks, Hkv, D)
     if dev_status is not None:
         _check_ints(dev_status, "dev_status", least=1)
-    dev = _one_device(("k", k), ("v", v), ("slots", slots), ("k_cache", k_cache), ("v_cache", v_cache),
-                      ("dev_status", dev_status))
+    dev = _same_device("k v slots k_cache v_cache dev_status", k, v, slots, k_cache, v_cache, dev_status)
     with _on_device(dev):
         rc = lib.fca_append_kv(k.data_ptr(), ks, v.data_ptr(), vs, slots.data_ptr(), T, num_blocks, Hkv, D,
                                k_cache.data_ptr(), v_cache.data_ptr(), _ptr(dev_status), _stream_handle(stream, dev))
@@ -499,7 +507,8 @@ def fca_chunk_attention(q, k_cache, v_cache, plan: "ChunkPlan", out, lse=None, s
     _check_bf16(out, "out", shape)
     _check_caches(k_cache, v_cache, plan.num_blocks, plan.num_kv_heads, plan.head_dim)
     _check_lse(lse, plan.num_tokens, plan.num_q_heads)
-    _plan_device(plan, ("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("out", out), ("lse", lse))
+    if _same_device("q k_cache v_cache out lse", q, k_cache, v_cache, out, lse) != plan.device:
+        _plan_device(plan, ("q", q))
     _check(lib.fca_chunk_attention(q.data_ptr(), stride, k_cache.data_ptr(), v_cache.data_ptr(), plan.handle,
                                    out.data_ptr(), _ptr(lse), float(scale), _stream_handle(stream, plan.device)), "fca_chunk_attention")
 

@@ -273,8 +273,10 @@ extern "C" fca_status fca_extend_tables(int32_t* block_tables, int32_t max_block
     a.num_blocks = num_blocks;
     a.num_slots = num_slots;
     const size_t smem = (3 * (size_t)num_requests + 1) * sizeof(int32_t);
-    cudaError_t e = cudaFuncSetAttribute(k_extend_tables, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)((3 * (size_t)kMaxRequests + 1) * sizeof(int32_t)));
+    // (only what the default limit does not cover asks for more)
+    cudaError_t e = smem <= 32 * 1024 ? cudaSuccess
+                                      : cudaFuncSetAttribute(k_extend_tables, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                             (int)((3 * (size_t)kMaxRequests + 1) * sizeof(int32_t)));
     if (note_cuda(e) != cudaSuccess) {
         (void)cudaGetLastError();
         return FCA_ERR_CUDA;
