@@ -244,6 +244,19 @@ __device__ __noinline__ void exact_row(const ChunkArgs& a, int32_t req, int32_t 
     }
 }
 
+// Whether V has an inf or NaN in tokens [tok0, tok1), by one warp.
+template <int D>
+__device__ __noinline__ bool v_not_finite(const ChunkArgs& a, int32_t req, int32_t head, int32_t tok0, int32_t tok1) {
+    float x = 0.f;
+    for (int32_t j = tok0; j < tok1; ++j) {
+        const int32_t b = a.bt[(int64_t)req * a.max_blocks + j / kBlockSize];
+        const int64_t at = (((int64_t)b * kBlockSize + j % kBlockSize) * a.Hkv + head) * D;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) x = fmaf(__bfloat162float(a.v[at + (threadIdx.x & 31) + 32 * i]), 0.f, x);
+    }
+    return __any_sync(0xffffffffu, isnan(x));
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     k_chunk(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
@@ -570,13 +583,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     a.lse[orow] = lw * kLn2;
             }
             // A product of weight 0 with an inf or NaN that the row does not see
-            // (a later token's) is NaN: rows that are not finite are computed
-            // again from the tokens that they do see.
+            // (a later token's) is NaN: a row that is not finite is computed again from
+            // the tokens that it does see, if V is not finite in one that it does not.
             uint32_t again = __ballot_sync(0xffffffffu, mine && isnan(finite));
             while (again) {
                 const int src = __ffs(again) - 1;
                 again &= again - 1;
                 const int ri = t * 128 + quarter * 32 + src;
+                if (!v_not_finite<D>(a, w.it.req, w.it.head, max(w.it.tok0, row_limit(a, w.it, ri)), w.it.tok1)) continue;
                 const int64_t r_out = __shfl_sync(0xffffffffu, orow, src), r_part = __shfl_sync(0xffffffffu, prow, src);
                 int32_t qh2;
                 const int32_t tok2 = row_token(a, w.it, ri, qh2);

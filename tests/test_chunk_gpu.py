@@ -309,6 +309,72 @@ def test_what_a_row_does_not_see_has_no_part_in_it():
         assert bool((off[early] <= 1).all())
 
 
+def test_what_a_row_does_see_stays_in_it():
+    # inf and NaN in tokens that every row sees: out is not finite there, elsewhere as ever
+    torch = _torch()
+    b = Batch([5000, 300], [70, 300], 8, 2, 128, seed=7)
+    v = b.v.view(-1, 2, 128)
+    v[b.slot[0][17], 0, 3] = float("nan")
+    v[b.slot[0][4000], 1, 9] = float("inf")
+    with b.plan() as plan:
+        b.attend(plan)
+    o = b.out[:70].float().view(70, 2, 4, 128)
+    bad = ~torch.isfinite(o)
+    want = torch.zeros_like(bad)
+    want[:, 0, :, 3] = True
+    want[:, 1, :, 9] = True
+    assert bool((bad == want).all())
+    assert bool((o[:, 1, :, 9] == float("inf")).all())
+    b.new_h[0] = 0
+    check(b, what="the request beside")
+
+
+def test_nothing_to_attend():
+    torch = _torch()
+    import shared_prefix_kv_fca_b200 as fca
+    for rows in (0, 5):                     # no rows at all, and rows that belong to no request
+        b = Batch([40, 0], [0, 0], 4, 1, 64, seed=1, pad_rows=rows)
+        with b.plan() as plan:
+            b.attend(plan)
+            plan.update(b.tables, b.seq, b.starts)
+            b.attend(plan)
+            assert fca.fca_chunk_check_status(plan) == 0
+        assert bool((b.out == 7.25).all()) and bool((b.lse == 7.25).all())
+
+
+def test_as_many_requests_as_there_may_be():
+    # 16384 requests: the sums' and the shared memory's full size
+    import random
+    import shared_prefix_kv_fca_b200 as fca
+    rng = random.Random(2)
+    had = [rng.choice([0, 15, 16, 31, 3]) for _ in range(16384)]
+    new = [rng.choice([0, 1, 1, 2]) for _ in had]
+    s, want = table_step(had, new, 4, seed=3, slots=sum(new) + 9)
+    got = run_tables(s, had, new)
+    for key in want:
+        assert got[key] == want[key], key
+    torch = _torch()
+    b = Batch([max(h + n, 1) for h, n in zip(had, new)], new, 2, 1, 64, seed=4)
+    with b.plan() as plan:
+        b.attend(plan)
+        assert fca.fca_chunk_check_status(plan) == 0
+    # every row at once: at most 33 tokens, gathered into a rectangle
+    lens = torch.tensor(b.seq_h, device="cuda")
+    owner = torch.repeat_interleave(torch.arange(16384, device="cuda"), torch.tensor(new, device="cuda"))
+    first = torch.tensor(b.starts_h[:-1], device="cuda")
+    pos = lens[owner] - torch.tensor(new, device="cuda")[owner] + torch.arange(b.T, device="cuda") - first[owner]
+    j = torch.arange(64, device="cuda")
+    slot = b.tables.long()[owner][:, (j // BLOCK).clamp(max=b.tables.shape[1] - 1)] * BLOCK + j % BLOCK
+    sees = j[None] <= pos[:, None]
+    slot = torch.where(sees, slot, slot[:, :1])
+    k, v = (c.view(-1, 64)[slot].double() for c in (b.k, b.v))
+    w = torch.einsum("thd,tld->thl", b.q.double(), k) * b.scale
+    w = torch.softmax(w.masked_fill(~sees[:, None], -math.inf), -1)
+    ref, a = torch.einsum("thl,tld->thd", w, v), torch.einsum("thl,tld->thd", w, v.abs())
+    off = (b.out.double() - ref).abs() / ((2.0 ** -7 + 2.0 ** -12) * a * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs())
+    assert bool((off <= 1).all()), off.max().item()
+
+
 def test_offsets_beyond_32_bits():
     torch = _torch()
     hkv, d = 8, 128
