@@ -76,9 +76,9 @@ struct ChunkArgs {
     float* lse;
     float* part_o;
     float* part_w;
-    int32_t part_rows, max_blocks, num_blocks, Hq, Hkv, G;
+    int32_t part_rows, max_blocks, num_blocks, T, Hq, Hkv, G;
     uint32_t div_g;     // 65536 / G, rounded up: x / G = x div_g >> 16 for x < kChunkRows + 16
-    int32_t q_tma;      // queries by TMA: G divides a tile
+    int32_t q_tma;      // queries by TMA, 16 stacked rows a box: G divides 16
     float scale_log2;
     int32_t* err;
 };
@@ -480,6 +480,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     dev::mbar_arrive(s_free);
                     ok = weights_free();
+                    if (ok && x == 0) {
+                        // what an earlier item left there is cleared, for the same reason as unused query rows
+                        uint32_t z[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) z[e] = 0u;
+                        dev::tmem_st32(p_addr, z);
+                        dev::tmem_st32(p_addr + 32, z);
+                        dev::tc_wait_st();
+                        dev::tc_fence_before();
+                    }
                     if (ok) dev::mbar_arrive(&p_full[t]);
                 }
             }
@@ -645,17 +655,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int b = 0; b < 2; ++b) {
                     uint32_t& n = b ? n_q1 : n_q0;
                     if (!ok || (b ? w.dual : w.ns0 == 0)) continue;
-                    if (n && !dev::mbar_wait(&q_free[b], (n - 1) & 1, abort_flag, a.err)) {
-                        ok = false;
-                        continue;
+                    if (lane == 0) {
+                        if (n && !dev::mbar_wait(&q_free[b], (n - 1) & 1, abort_flag, a.err))
+                            ok = false;
+                        else
+                            dev::mbar_arrive_expect_tx(&q_full[b], L::kTileQ);
                     }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) continue;
                     ++n;
-                    // (rows behind the request's are other requests' queries: computed like
-                    // the others and left alone)
-                    dev::mbar_arrive_expect_tx(&q_full[b], L::kTileQ);
-                    for (int hf = 0; hf < L::kHalves; ++hf)
-                        dev::tma_load_3d(smem + L::kOffQ + b * L::kTileQ + hf * (128 * 128), &tmQ, &q_full[b], hf * 64,
-                                         w.it.head * a.G, w.it.q0 + over_g(a, b * 128));
+                    // Lane e < 8 loads stacked rows 16 e on.  Boxes without a row of the item are
+                    // loaded from rows beyond q, as zeros: products with zeros draw less
+                    // power, and the step runs at the clock that power leaves.
+                    if (lane < 8) {
+                        const int32_t r0 = (w.dual ? 0 : b * 128) + 16 * lane;
+                        const int32_t tok = r0 < w.it.nrows ? w.it.q0 + over_g(a, r0) : a.T;
+                        for (int hf = 0; hf < L::kHalves; ++hf)
+                            dev::tma_load_3d(smem + L::kOffQ + b * L::kTileQ + hf * (128 * 128) + lane * (16 * 128), &tmQ,
+                                             &q_full[b], hf * 64, w.it.head * a.G, tok);
+                    }
                 }
             };
             Work nw = load_work(a, first);
@@ -668,8 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     nxt = fetch(nw, 0);             // the next item's first batch, while this one streams
                 }
                 int32_t more = w.ns > kStagesPerBatch ? fetch(w, 1) : 0;
-                if (!is_k && a.q_tma && w.ns && lane == 0) load_q(w);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!is_k && a.q_tma && w.ns) load_q(w);
                 if (!ok) break;
                 for (int32_t j = 0; j < w.ns; ++j, ++g) {
                     if (j && j % kStagesPerBatch == 0) {
@@ -929,6 +946,7 @@ extern "C" fca_status fca_chunk_attention(const void* q, int64_t q_row_stride, c
     a.part_rows = plan->part_rows;
     a.max_blocks = plan->max_blocks;
     a.num_blocks = plan->num_blocks;
+    a.T = plan->T;
     a.Hq = plan->Hq;
     a.Hkv = plan->Hkv;
     a.G = plan->G;
@@ -936,8 +954,8 @@ extern "C" fca_status fca_chunk_attention(const void* q, int64_t q_row_stride, c
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err = plan->dev_status;
     CUtensorMap tq = tk;
-    a.q_tma = 128 % plan->G == 0;
-    if (a.q_tma && !make_rows_map(&tq, q, plan->T, plan->Hq, plan->D, q_row_stride, plan->G, 128 / plan->G)) return FCA_ERR_CUDA;
+    a.q_tma = 16 % plan->G == 0;
+    if (a.q_tma && !make_rows_map(&tq, q, plan->T, plan->Hq, plan->D, q_row_stride, plan->G, 16 / plan->G)) return FCA_ERR_CUDA;
     const cudaError_t e = plan->D == 128 ? launch_chunk<128>(a, tk, tv, tq, plan->ctas, s) : launch_chunk<64>(a, tk, tv, tq, plan->ctas, s);
     if (note_cuda(e) != cudaSuccess) return FCA_ERR_CUDA;
     if (plan->may_cut) {
