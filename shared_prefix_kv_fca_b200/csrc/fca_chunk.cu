@@ -4,40 +4,56 @@
 // Row (token t of request r, query head h) at position p = L - n + i:
 //   s_j = scale q.k_j,  o = sum_{j <= p} exp(s_j - m) v_j / sum_j exp(s_j - m),
 //   lse = m + log sum_j exp(s_j - m)
-// over the cached tokens j that the row sees (all L of them in full plans), in one pass
-// over the tokens with a running reference m and running sums.
+// over the cached tokens j that the row sees (all L of them in full plans), in one
+// pass over the tokens with a running reference m and running sums.
 //
 // The rows of a request that read one KV head (tokens x query heads of the
 // group) are stacked, so that a K or V stage in shared memory serves them
 // all.  A CTA walks its items of the plan (fca_chunk_plan.cu); an item is up to
 // 256 stacked rows against a range of tokens, 128 tokens a stage:
 //   - above 128 rows: two MMA tiles of 128 rows share every stage, each with its
-//     own scores, weights and accumulator, so that the softmax of one tile runs
-//     while the tensor core works for the other;
-//   - up to 128 rows: one tile's rows, but its even and odd stages go to the two
-//     halves of the machinery, whose two accumulators are joined at the end: few rows are bound by
-//     the cache's bytes, and the softmax of a stage (a row is one thread) takes
-//     longer than its bytes.
+//     own weights and accumulator, so that the softmax of one tile runs while
+//     the tensor core works for the other;
+//   - up to 128 rows ("dual"): one tile's rows, but its even and odd stages go
+//     to the two halves of the machinery, whose accumulators are joined at
+//     the end: few rows are bound by the cache's bytes, and the softmax of a
+//     stage (a row is one thread) takes longer than the bytes do.
 //
 // 384 threads:
-//   warps 0-3, 4-7  the warpgroups of tile 0 and tile 1, one thread a row: load the
-//                tile's queries, then for each stage read the scores from tensor memory
-//                into registers and write the weights back as bf16; the
-//                accumulator is rescaled in place in the rare case that a row's maximum
+//   warps 0-3, 4-7  the warpgroups of tile 0 and tile 1, one thread a row: for
+//                each stage they read the scores from tensor memory into
+//                registers and write the weights back as bf16; the accumulator is
+//                rescaled in place in the rare case that a row's maximum
 //                outgrows its reference; at the item's end they normalise and store;
-//   warps 8, 9   TMA loads of K and V, one block of 16 tokens a box;
+//   warps 8, 9   TMA loads of K, and of V and the queries; one block of 16
+//                tokens, or 16 stacked query rows, a box;
 //   warps 10, 11 MMA issue: S = Q K^T (operands in shared memory), and
 //                O += P V (P from tensor memory).
 // Tensor memory holds one score buffer, two weight buffers and two
 // accumulators.  The tiles take turns with the scores: a softmax warp copies its
 // row of 128 scores to registers and gives the buffer up before it computes
 // anything, so that the other tile's Q K^T, and this tile's next, never wait for an
-// exponential or a P V, and scores are there when a tile has finished a stage.
-// (With a score buffer per tile and the weights written over the scores, a tile's next
-// Q K^T had to wait for its P V: 5300 cycles a stage of 256 x 128 instead of 3100.)
+// exponential or a P V.  (With a score buffer per tile and the weights
+// written over the scores, a tile's next Q K^T had to wait for its P V:
+// 5300 cycles a stage of 256 x 128 instead of 3300.)
+//
+// What bounds it.  A stage of 256 x 128 at head_dim 128 needs 2048 tensor cycles,
+// 2048 cycles of exponentials (16 a cycle and SM) and 2048 of shared-memory reads,
+// and takes 3300: the softmax of the two tiles, two warps a scheduler, takes 2350
+// by itself, and what the tiles wait for each other does the rest.  Measured: 4096 tokens
+// behind 32768 (32/8/128) 1.9 ms, 1230 TFLOP/s (74% of the measured burst rate; 2.2 ms in
+// runs of seconds, at the clock that power leaves); 16 prompts of 2048 600 us,
+// 920 TFLOP/s: an item's start and end cost 3.5 us.  Dual items are
+// bound by the cache's bytes: 96 decodes 5.5 TB/s (84% of the copy rate), 64 x 5
+// drafted tokens 5.2 TB/s.  Tried and slower: exponentials partly by a polynomial on the FMA
+// pipe; 16 softmax warps of 64 columns; one warp issuing both products in
+// order; a second score buffer at head_dim 64; P handed over in halves.
+//
 // Every wait is bounded (fca_device.cuh); a role that gives up sets the CTA's
 // abort flag, the others leave at their next wait, copies and MMAs in flight
-// are waited for, and tensor memory is freed.
+// are waited for, and tensor memory is freed.  A parity tells a phase from the
+// next one only: whoever waits on a barrier either holds its next phase up or
+// is the only one to wait, so that none can fall two phases behind.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -894,7 +910,8 @@ __global__ void __launch_bounds__(kMergeThreads) k_chunk_merge(ChunkArgs a, cons
 }
 
 template <int D>
-cudaError_t launch_chunk(const ChunkArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq, int ctas, cudaStream_t stream) {
+cudaError_t launch_chunk(const ChunkArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq, int ctas,
+                         cudaStream_t stream) {
     using L = Layout<D>;
     // setmaxnreg hands out what the block was launched with: it has to have been kRegsLaunch a thread
     static const cudaError_t ready = [] {
@@ -956,7 +973,8 @@ extern "C" fca_status fca_chunk_attention(const void* q, int64_t q_row_stride, c
     CUtensorMap tq = tk;
     a.q_tma = 16 % plan->G == 0;
     if (a.q_tma && !make_rows_map(&tq, q, plan->T, plan->Hq, plan->D, q_row_stride, plan->G, 16 / plan->G)) return FCA_ERR_CUDA;
-    const cudaError_t e = plan->D == 128 ? launch_chunk<128>(a, tk, tv, tq, plan->ctas, s) : launch_chunk<64>(a, tk, tv, tq, plan->ctas, s);
+    const cudaError_t e = plan->D == 128 ? launch_chunk<128>(a, tk, tv, tq, plan->ctas, s)
+                                         : launch_chunk<64>(a, tk, tv, tq, plan->ctas, s);
     if (note_cuda(e) != cudaSuccess) return FCA_ERR_CUDA;
     if (plan->may_cut) {
         // set up while the tiles run, which it waits for
