@@ -976,7 +976,13 @@ extern "C" fca_status fca_chunk_attention(const void* q, int64_t q_row_stride, c
     const cudaError_t e = plan->D == 128 ? launch_chunk<128>(a, tk, tv, tq, plan->ctas, s)
                                          : launch_chunk<64>(a, tk, tv, tq, plan->ctas, s);
     if (note_cuda(e) != cudaSuccess) return FCA_ERR_CUDA;
-    if (plan->may_cut) {
+    // A captured attention may run after updates that cut tiles where there are none now.
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (!plan->may_cut && cudaStreamIsCapturing(s, &capture) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return FCA_ERR_CUDA;
+    }
+    if (plan->may_cut || capture != cudaStreamCaptureStatusNone) {
         // set up while the tiles run, which it waits for
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3(plan->ctas, kMergeSplit);

@@ -55,7 +55,7 @@ struct fca_chunk_plan_s {
     int32_t R = 0, T = 0, max_blocks = 0, num_blocks = 0;
     int32_t Hq = 0, Hkv = 0, D = 0, G = 0;
     bool full = false;
-    bool may_cut = true;            // whether the lists may hold cut tiles (known after a synchronous build)
+    bool may_cut = true;            // whether the lists hold cut tiles, as far as the host knows
     int32_t ctas = 0;               // CTAs the lists are made for
     int32_t part_rows = 0;          // partial rows a slot
     int64_t cap_items = 0;

@@ -438,6 +438,30 @@ def test_a_plan_updated_and_captured():
     plan.close()
 
 
+def test_a_captured_attention_runs_after_updates_outside_the_graph():
+    # the plan has no cut tiles when the graph is made, and has some when it is replayed
+    torch = _torch()
+    import shared_prefix_kv_fca_b200 as fca
+    b = Batch([9000, 40], [3, 2], 8, 2, 128, seed=21)
+    short = torch.tensor([3, 2], dtype=torch.int32, device="cuda")
+    with fca.fca_chunk_plan(b.tables, short, b.starts, b.T, b.pool, b.hq, b.hkv, b.d) as plan:
+        side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            b.attend(plan)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side, capture_error_mode="thread_local"):
+            b.attend(plan)
+        plan.update(b.tables, b.seq, b.starts)
+        b.out.fill_(7.25)
+        b.lse.fill_(7.25)
+        graph.replay()
+        torch.cuda.synchronize()
+        check(b, what="replayed")
+        assert fca.fca_chunk_check_status(plan) == 0
+        del graph
+
+
 def test_bad_steps_are_refused_or_flagged():
     torch = _torch()
     import shared_prefix_kv_fca_b200 as fca
