@@ -227,39 +227,6 @@ __device__ __forceinline__ void weights32(const uint32_t (&x)[32], float2 sc, fl
     }
 }
 
-// One row by one warp with plain arithmetic, lane i holding D / 32 of the
-// row's elements: o unnormalised, against the row's maximum m, and the sum l.
-template <int D>
-__device__ __noinline__ void exact_row(const ChunkArgs& a, int32_t req, int32_t head, const __nv_bfloat16* q, int32_t tok0,
-                                       int32_t tok1, float (&o)[D / 32], float& m, float& l) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    float qf[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        qf[i] = __bfloat162float(q[lane * E + i]);
-        o[i] = 0.f;
-    }
-    m = -INFINITY;
-    l = 0.f;
-    for (int32_t j = tok0; j < tok1; ++j) {
-        const int32_t b = a.bt[(int64_t)req * a.max_blocks + j / kBlockSize];
-        const int64_t at = (((int64_t)b * kBlockSize + j % kBlockSize) * a.Hkv + head) * D + lane * E;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) s += qf[i] * __bfloat162float(a.k[at + i]);
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= a.scale_log2;
-        const float top = fmaxf(m, s);
-        const float f = top == -INFINITY ? 1.f : exp2f(m - top), p = top == -INFINITY ? exp2f(s) : exp2f(s - top);
-        m = top;
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < E; ++i) o[i] = o[i] * f + p * __bfloat162float(a.v[at + i]);
-    }
-}
-
 // Whether V has an inf or NaN in tokens [tok0, tok1), by one warp.
 template <int D>
 __device__ __noinline__ bool v_not_finite(const ChunkArgs& a, int32_t req, int32_t head, int32_t tok0, int32_t tok1) {
@@ -271,6 +238,122 @@ __device__ __noinline__ bool v_not_finite(const ChunkArgs& a, int32_t req, int32
         for (int i = 0; i < D / 32; ++i) x = fmaf(__bfloat162float(a.v[at + (threadIdx.x & 31) + 32 * i]), 0.f, x);
     }
     return __any_sync(0xffffffffu, isnan(x));
+}
+
+// Rows row0 + i of item `item`, for the bits i of `rows`, by one warp with plain arithmetic, from the
+// tokens that they see; the results are written over what is there.  Does nothing where V is finite
+// in all that some of them do not see: then they are what they should be.  Other roles
+// wait meanwhile, no longer than their limit, so rows are taken kExactRows at a time and tokens 32
+// at a time, a lane a token for the scores: 64 rows of 30000 tokens on every SM at once
+// take 48 ms (512 ms a row at a time).
+constexpr int kExactRows = 8;
+
+template <int D>
+__device__ __noinline__ void exact_rows(const ChunkArgs& a, int32_t item, int row0, uint32_t rows) {
+    constexpr int E = D / 32, N = kExactRows;
+    const int lane = threadIdx.x & 31;
+    const ChunkItem it = load_work(a, item).it;
+    if (!v_not_finite<D>(a, it.req, it.head, max(it.tok0, row_limit(a, it, row0 + __ffs(rows) - 1)), it.tok1)) return;
+    while (rows) {
+        int r[N];                               // (the last one again where there are fewer)
+        int32_t lim[N];
+        const __nv_bfloat16* q[N];
+        float o[N][E], m[N], l[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if (rows) r[k] = row0 + __ffs(rows) - 1;
+            else if (k > 0) r[k] = r[k - 1];
+            rows &= rows - 1;
+            lim[k] = row_limit(a, it, r[k]);
+            int32_t qhead;
+            const int32_t tok = row_token(a, it, r[k], qhead);
+            q[k] = a.q + (int64_t)tok * a.q_stride + qhead * D;
+            m[k] = -INFINITY;
+            l[k] = 0.f;
+#pragma unroll
+            for (int i = 0; i < E; ++i) o[k][i] = 0.f;
+        }
+        const int32_t end = lim[N - 1];         // limits grow with the row
+        for (int32_t j0 = it.tok0; j0 < end; j0 += 32) {
+            const int32_t j = min(j0 + lane, end - 1);
+            const int32_t b = a.bt[(int64_t)it.req * a.max_blocks + j / kBlockSize];
+            const int64_t at = (((int64_t)b * kBlockSize + j % kBlockSize) * a.Hkv + it.head) * D;
+            float s[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) s[k] = 0.f;
+#pragma unroll 4
+            for (int c = 0; c < D / 8; ++c) {
+                const uint4 kx = *reinterpret_cast<const uint4*>(a.k + at + c * 8);
+                const uint32_t kw[4] = {kx.x, kx.y, kx.z, kx.w};
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const uint4 qx = *reinterpret_cast<const uint4*>(q[k] + c * 8);
+                    const uint32_t qw[4] = {qx.x, qx.y, qx.z, qx.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[k] = fmaf(as_f(kw[e] << 16), as_f(qw[e] << 16), s[k]);
+                        s[k] = fmaf(as_f(kw[e] & 0xffff0000u), as_f(qw[e] & 0xffff0000u), s[k]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                s[k] = j0 + lane < lim[k] ? s[k] * a.scale_log2 : -INFINITY;
+                float top = s[k];
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                top = fmaxf(m[k], top);
+                const float ref = top == -INFINITY ? 0.f : top, f = exp2f(m[k] - ref);
+                s[k] = exp2f(s[k] - ref);       // the token's weight
+                m[k] = top;
+                float sum = s[k];
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                l[k] = l[k] * f + sum;
+#pragma unroll
+                for (int i = 0; i < E; ++i) o[k][i] *= f;
+            }
+            const int n = min(32, end - j0);
+#pragma unroll 4
+            for (int y = 0; y < n; ++y) {
+                const __nv_bfloat16* v = a.v + __shfl_sync(0xffffffffu, at, y) + lane * E;
+                float vf[E];
+#pragma unroll
+                for (int i = 0; i < E; i += 2) {
+                    const uint32_t vx = *reinterpret_cast<const uint32_t*>(v + i);
+                    vf[i] = as_f(vx << 16);
+                    vf[i + 1] = as_f(vx & 0xffff0000u);
+                }
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const float w = __shfl_sync(0xffffffffu, s[k], y);
+#pragma unroll
+                    for (int i = 0; i < E; ++i) o[k][i] = j0 + y < lim[k] ? fmaf(w, vf[i], o[k][i]) : o[k][i];
+                }
+            }
+        }
+        __syncwarp();                           // behind what the rows' own lanes wrote
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            int32_t qhead;
+            const int32_t tok = row_token(a, it, r[k], qhead);
+            const int64_t orow = (int64_t)tok * a.Hq + qhead, prow = (int64_t)it.slot * a.part_rows + r[k];
+            const float inv = l[k] == 0.f ? 0.f : 1.f / l[k], lw = m[k] + log2f(l[k]);
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                if (it.slot < 0)
+                    a.out[orow * D + lane * E + i] = __float2bfloat16(o[k][i] * inv);
+                else
+                    a.part_o[prow * D + lane * E + i] = o[k][i] * inv;
+            }
+            if (lane == 0) {
+                if (it.slot >= 0)
+                    a.part_w[prow] = lw;
+                else if (a.lse)
+                    a.lse[orow] = lw * kLn2;
+            }
+        }
+    }
 }
 
 template <int D>
@@ -611,36 +694,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // A product of weight 0 with an inf or NaN that the row does not see
             // (a later token's) is NaN: a row that is not finite is computed again from
             // the tokens that it does see, if V is not finite in one that it does not.
-            uint32_t again = __ballot_sync(0xffffffffu, mine && isnan(finite));
-            while (again) {
-                const int src = __ffs(again) - 1;
-                again &= again - 1;
-                const int ri = t * 128 + quarter * 32 + src;
-                if (!v_not_finite<D>(a, w.it.req, w.it.head, max(w.it.tok0, row_limit(a, w.it, ri)), w.it.tok1)) continue;
-                const int64_t r_out = __shfl_sync(0xffffffffu, orow, src), r_part = __shfl_sync(0xffffffffu, prow, src);
-                int32_t qh2;
-                const int32_t tok2 = row_token(a, w.it, ri, qh2);
-                float o[D / 32], me, le;
-                exact_row<D>(a, w.it.req, w.it.head, a.q + (int64_t)tok2 * a.q_stride + qh2 * D, w.it.tok0,
-                             row_limit(a, w.it, ri), o, me, le);
-                const float scale = le == 0.f ? 0.f : 1.f / le;
-                __syncwarp();
-#pragma unroll
-                for (int e = 0; e < D / 32; ++e) {
-                    const int col = lane * (D / 32) + e;
-                    if (whole)
-                        a.out[r_out * D + col] = __float2bfloat16(o[e] * scale);
-                    else
-                        a.part_o[r_part * D + col] = o[e] * scale;
-                }
-                if (lane == 0) {
-                    const float lr = me + log2f(le);
-                    if (!whole)
-                        a.part_w[r_part] = lr;
-                    else if (a.lse)
-                        a.lse[r_out] = lr * kLn2;
-                }
-            }
+            const uint32_t again = __ballot_sync(0xffffffffu, mine && isnan(finite));
+            if (again) exact_rows<D>(a, i, t * 128 + quarter * 32, again);
         }
     } else {
         regs_dec<kRegsOthers>();

@@ -309,6 +309,19 @@ def test_what_a_row_does_not_see_has_no_part_in_it():
         assert bool((off[early] <= 1).all())
 
 
+def test_what_rows_do_not_see_behind_a_long_cache():
+    # the last token's value is not finite: the rows before it are computed again, from all of a
+    # long cache, of which a CTA has as much as 30000 tokens
+    _torch()
+    import shared_prefix_kv_fca_b200 as fca
+    b = Batch([30000], [64], 592, 148, 64, seed=22)
+    b.v.view(-1, 148, 64)[b.slot[0][-1], :, 50] = float("nan")
+    with b.plan() as plan:
+        b.attend(plan)
+        assert fca.fca_chunk_check_status(plan) == 0
+        check(b, what="one value at the end")
+
+
 def test_what_a_row_does_see_stays_in_it():
     # inf and NaN in tokens that every row sees: out is not finite there, elsewhere as ever
     torch = _torch()
