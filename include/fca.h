@@ -403,7 +403,7 @@ fca_status fca_paged_decode_static(const void *q, const void *k_cache, const voi
  *
  * Returns FCA_ERR_INVALID_ARG (null or misaligned pointer, bad shape, buffers
  * that overlap otherwise than stated, as far as seq_lens and cached_lens
- * do), FCA_ERR_UNSUPPORTED (over 16384 requests, or
+ * do), FCA_ERR_UNSUPPORTED (over 16384 requests or 2^30 slots, or
  * num_blocks or max_blocks beyond 2^31 / 16), FCA_ERR_CUDA.  num_requests == 0
  * sets q_starts[0] to 0, the slots to -1 and free_after.  Asynchronous on
  * `stream`, one kernel or two, no workspace; runs on the current device.
@@ -423,8 +423,8 @@ fca_status fca_extend_tables(int32_t *block_tables, int32_t max_blocks, const in
  *            sit in a wider projection output).
  *   slots    DEVICE int32 [num_tokens]: row i goes to token slots[i] % 16 of
  *            block slots[i] / 16; a negative slot skips the row.  A slot of
- *            num_blocks * 16 or more skips the row too and sets bit 16.  Two
- *            rows with one slot leave either of them there.
+ *            num_blocks * 16 or more skips the row too and sets bit 16.  Of two
+ *            rows with one slot, each 16 bytes there may come from either.
  *   k_cache, v_cache  DEVICE bf16 [num_blocks][16][num_kv_heads][head_dim],
  *            16-byte aligned, not overlapping k or v.
  *   dev_status  DEVICE int32, or NULL: error bits are ORed into it.

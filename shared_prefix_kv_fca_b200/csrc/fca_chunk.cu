@@ -55,6 +55,7 @@
 // next one only: whoever waits on a barrier either holds its next phase up or
 // is the only one to wait, so that none can fall two phases behind.
 #include <algorithm>
+#include <atomic>
 
 #include <cuda_bf16.h>
 
@@ -969,13 +970,15 @@ cudaError_t launch_chunk(const ChunkArgs& a, const CUtensorMap& tk, const CUtens
                          cudaStream_t stream) {
     using L = Layout<D>;
     // setmaxnreg hands out what the block was launched with: it has to have been kRegsLaunch a thread
-    static const cudaError_t ready = [] {
+    static std::atomic<bool> checked{false};
+    cudaError_t e;
+    if (!checked) {
         cudaFuncAttributes at{};
-        cudaError_t r = cudaFuncGetAttributes(&at, k_chunk<D>);
-        return r == cudaSuccess && at.numRegs != kRegsLaunch ? cudaErrorInvalidConfiguration : r;
-    }();
-    if (ready != cudaSuccess) return ready;
-    cudaError_t e = cudaFuncSetAttribute(k_chunk<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
+        if ((e = cudaFuncGetAttributes(&at, k_chunk<D>)) != cudaSuccess) return e;
+        if (at.numRegs != kRegsLaunch) return cudaErrorInvalidConfiguration;
+        checked = true;
+    }
+    e = cudaFuncSetAttribute(k_chunk<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
     k_chunk<D><<<ctas, kThreads, L::kAlloc, stream>>>(a, tk, tv, tq);
     return cudaGetLastError();

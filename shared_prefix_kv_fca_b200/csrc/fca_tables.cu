@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWide = 4;        // tokens a lane has under way at once
+constexpr int32_t kMaxSlots = 1 << 30;      // (places of slots are added to in 32 bits)
 
 struct TablesArgs {
     int32_t* bt;
@@ -254,7 +255,7 @@ extern "C" fca_status fca_extend_tables(int32_t* block_tables, int32_t max_block
     if (seq_lens != cached_lens && overlap(seq_lens, 4 * (size_t)num_requests, cached_lens, 4 * (size_t)num_requests))
         return FCA_ERR_INVALID_ARG;
     if (num_requests > kMaxRequests || (int64_t)num_blocks * kBlockSize > INT32_MAX ||
-        (int64_t)max_blocks * kBlockSize > INT32_MAX)
+        (int64_t)max_blocks * kBlockSize > INT32_MAX || num_slots > kMaxSlots)
         return FCA_ERR_UNSUPPORTED;
     TablesArgs a;
     a.bt = block_tables;

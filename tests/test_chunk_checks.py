@@ -178,7 +178,7 @@ def test_entry_points_check_before_the_device():
         a = list(good)
         a[at] = v
         assert lib.fca_extend_tables(*a) == 1, (at, v)
-    for at, v in ((4, 16385), (8, 1 << 27), (1, 1 << 27)):
+    for at, v in ((4, 16385), (8, 1 << 27), (1, 1 << 27), (12, (1 << 30) + 1)):
         a = list(good)
         a[at] = v
         assert lib.fca_extend_tables(*a) == 3, (at, v)
