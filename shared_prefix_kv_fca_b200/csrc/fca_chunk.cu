@@ -44,8 +44,8 @@
 // behind 32768 (32/8/128) 1.9 ms, 1230 TFLOP/s (74% of the measured burst rate; 2.2 ms in
 // runs of seconds, at the clock that power leaves); 16 prompts of 2048 600 us,
 // 920 TFLOP/s: an item's start and end cost 3.5 us.  Dual items are
-// bound by the cache's bytes: 96 decodes 5.5 TB/s (84% of the copy rate), 64 x 5
-// drafted tokens 5.2 TB/s.  Tried and slower: exponentials partly by a polynomial on the FMA
+// bound by the cache's bytes: 192 x 5 drafted tokens (3.8 GB) 6.5 TB/s, 99% of the copy
+// rate; 64 x 5 (0.85 GB) 5.3 TB/s, with 15 us of start and end.  Tried and slower: exponentials partly by a polynomial on the FMA
 // pipe; 16 softmax warps of 64 columns; one warp issuing both products in
 // order; a second score buffer at head_dim 64; P handed over in halves.
 //
