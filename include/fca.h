@@ -401,9 +401,8 @@ fca_status fca_paged_decode_static(const void *q, const void *k_cache, const voi
  * cached_lens, free_after free_next, q_starts 0 and every slot -1, so that
  * the calls that follow have no new tokens.
  *
- * Returns FCA_ERR_INVALID_ARG (null or misaligned pointer, bad shape, buffers
- * that overlap otherwise than stated, as far as seq_lens and cached_lens
- * do), FCA_ERR_UNSUPPORTED (over 16384 requests or 2^30 slots, or
+ * Returns FCA_ERR_INVALID_ARG (null or misaligned pointer, bad shape, an output
+ * that overlaps another buffer otherwise than stated), FCA_ERR_UNSUPPORTED (over 16384 requests or 2^30 slots, or
  * num_blocks or max_blocks beyond 2^31 / 16), FCA_ERR_CUDA.  num_requests == 0
  * sets q_starts[0] to 0, the slots to -1 and free_after.  Asynchronous on
  * `stream`, one kernel or two, no workspace; runs on the current device.

@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend_lengths(TablesArgs a) {
 
 bool overlap(const void* p, size_t np, const void* q, size_t nq) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return a < b + nq && b < a + np;
+    return np && nq && a < b + nq && b < a + np;
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -252,11 +252,20 @@ extern "C" fca_status fca_extend_tables(int32_t* block_tables, int32_t max_block
                           (const void*)free_blocks, (const void*)free_next, (const void*)seq_lens,
                           (const void*)q_starts, (const void*)slots, (const void*)free_after, (const void*)dev_status})
         if (!aligned4(p)) return FCA_ERR_INVALID_ARG;
-    if (seq_lens != cached_lens && overlap(seq_lens, 4 * (size_t)num_requests, cached_lens, 4 * (size_t)num_requests))
-        return FCA_ERR_INVALID_ARG;
     if (num_requests > kMaxRequests || (int64_t)num_blocks * kBlockSize > INT32_MAX ||
         (int64_t)max_blocks * kBlockSize > INT32_MAX || num_slots > kMaxSlots)
         return FCA_ERR_UNSUPPORTED;
+    // What one CTA writes others may still have to read: outputs, the first six, stand alone.
+    const size_t r = (size_t)num_requests;
+    const struct { const int32_t* at; size_t n; } buf[10] = {
+        {block_tables, r * max_blocks}, {seq_lens, r}, {q_starts, r + 1}, {slots, (size_t)num_slots},
+        {free_after, 1}, {dev_status, dev_status ? 1u : 0u}, {cached_lens, r}, {new_lens, r},
+        {free_blocks, (size_t)num_free}, {free_next, 1}};
+    for (int x = 0; x < 6; ++x)
+        for (int y = x + 1; y < 10; ++y) {
+            const bool in_place = buf[x].at == buf[y].at && ((x == 1 && y == 6) || (x == 4 && y == 9));
+            if (!in_place && overlap(buf[x].at, 4 * buf[x].n, buf[y].at, 4 * buf[y].n)) return FCA_ERR_INVALID_ARG;
+        }
     TablesArgs a;
     a.bt = block_tables;
     a.cached = cached_lens;

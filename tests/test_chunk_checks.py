@@ -212,3 +212,22 @@ def test_entry_points_check_before_the_device():
     assert lib.fca_chunk_attention(p, 64, p, p, n, p, n, 0.1, n) == 1
     assert lib.fca_chunk_check_status(n, n, None) == 1
     assert lib.fca_chunk_plan_destroy(n) == 0
+
+
+def test_outputs_that_overlap_other_buffers_are_refused():
+    fbuild.build()
+    lib = fca.load_library()
+    at = [None] + [i << 16 for i in range(1, 11)]       # never dereferenced
+    #      bt     mb cached new   R  free  nf  next  NB  seq    starts slots  ns after  status stream
+    good = [at[1], 4, at[2], at[3], 5, at[4], 8, at[5], 8, at[6], at[7], at[8], 9, at[9], at[10], None]
+    sizes = {0: 20, 2: 5, 3: 5, 5: 8, 7: 1, 9: 5, 10: 6, 11: 9, 13: 1, 14: 1}
+    outputs = (0, 9, 10, 11, 13, 14)
+    for x in outputs:
+        for y in sizes:
+            if x == y:
+                continue
+            a = list(good)
+            a[x] = a[y] + 4 * (sizes[y] - 1)            # on the other's last element
+            if a[x] == a[y] and (x, y) == (13, 7):
+                continue                                # the list position may be updated in place
+            assert lib.fca_extend_tables(*a) == 1, (x, y)
