@@ -425,7 +425,7 @@ fca_status fca_extend_tables(int32_t *block_tables, int32_t max_blocks, const in
  *            num_blocks * 16 or more skips the row too and sets bit 16.  Of two
  *            rows with one slot, each 16 bytes there may come from either.
  *   k_cache, v_cache  DEVICE bf16 [num_blocks][16][num_kv_heads][head_dim],
- *            16-byte aligned, not overlapping k or v.
+ *            16-byte aligned, not overlapping k, v, slots or one another.
  *   dev_status  DEVICE int32, or NULL: error bits are ORed into it.
  *
  * Returns FCA_ERR_INVALID_ARG, FCA_ERR_UNSUPPORTED (head_dim not 64 or 128,
@@ -499,9 +499,9 @@ fca_status fca_chunk_plan_update(fca_chunk_plan_t plan, const int32_t *block_tab
  *            aligned, q_row_stride elements apart (a multiple of 8, at least
  *            num_q_heads * head_dim).
  *   k_cache, v_cache, scale  as fca_decode.
- *   out      DEVICE bf16 [num_tokens][num_q_heads][head_dim], 16-byte aligned; not
- *            overlapping q.
+ *   out      DEVICE bf16 [num_tokens][num_q_heads][head_dim], 16-byte aligned.
  *   lse      DEVICE fp32 [num_tokens][num_q_heads], or NULL.
+ *            Neither may overlap another buffer (q is read to the end): FCA_ERR_INVALID_ARG.
  *
  * Asynchronous on `stream`.  Uses the plan's workspace: attentions that share
  * a plan must be ordered.  The result of a row does not depend on timing: the same call on

@@ -75,6 +75,12 @@ extern "C" fca_status fca_append_kv(const void* k, int64_t k_row_stride, const v
     if (k_row_stride < row || v_row_stride < row || k_row_stride % 8 != 0 || v_row_stride % 8 != 0)
         return FCA_ERR_INVALID_ARG;
     if (num_tokens == 0) return FCA_OK;
+    const size_t cache = (size_t)num_blocks * kBlockSize * row * 2, n = (size_t)num_tokens - 1;
+    if (overlap(k_cache, cache, v_cache, cache)) return FCA_ERR_INVALID_ARG;
+    for (const void* c : {k_cache, v_cache})
+        if (overlap(c, cache, k, (n * k_row_stride + row) * 2) || overlap(c, cache, v, (n * v_row_stride + row) * 2) ||
+            overlap(c, cache, slots, 4 * (n + 1)))
+            return FCA_ERR_INVALID_ARG;
     AppendArgs a;
     a.k = static_cast<const uint4*>(k);
     a.v = static_cast<const uint4*>(v);

@@ -998,6 +998,15 @@ extern "C" fca_status fca_chunk_attention(const void* q, int64_t q_row_stride, c
         q_row_stride < (int64_t)plan->Hq * plan->D)
         return FCA_ERR_INVALID_ARG;
     if (plan->T == 0) return FCA_OK;
+    // q is read while rows of out and lse are written already
+    const size_t rows = (size_t)plan->T, heads = rows * plan->Hq;
+    const size_t cache = (size_t)plan->num_blocks * kBlockSize * plan->Hkv * plan->D * 2;
+    const size_t n_out = heads * plan->D * 2, n_lse = lse ? heads * 4 : 0;
+    const size_t n_q = ((rows - 1) * q_row_stride + (size_t)plan->Hq * plan->D) * 2;
+    if (overlap(out, n_out, lse, n_lse)) return FCA_ERR_INVALID_ARG;
+    for (const void* in : {q, k_cache, v_cache})
+        if (overlap(in, in == q ? n_q : cache, out, n_out) || overlap(in, in == q ? n_q : cache, lse, n_lse))
+            return FCA_ERR_INVALID_ARG;
     DeviceGuard dg(plan->device);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CUtensorMap tk, tv;

@@ -138,6 +138,12 @@ struct DeviceGuard {
     }
 };
 
+// Whether np bytes at p and nq bytes at q share one.
+inline bool overlap(const void* p, size_t np, const void* q, size_t nq) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return np && nq && a < b + nq && b < a + np;
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace fca

@@ -227,11 +227,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_extend_lengths(TablesArgs a) {
     if (threadIdx.x == 0) *a.free_after = *a.free_next + (int32_t)all;
 }
 
-bool overlap(const void* p, size_t np, const void* q, size_t nq) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return np && nq && a < b + nq && b < a + np;
-}
-
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace

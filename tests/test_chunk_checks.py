@@ -231,3 +231,15 @@ def test_outputs_that_overlap_other_buffers_are_refused():
             if a[x] == a[y] and (x, y) == (13, 7):
                 continue                                # the list position may be updated in place
             assert lib.fca_extend_tables(*a) == 1, (x, y)
+
+
+def test_caches_that_overlap_rows_are_refused():
+    fbuild.build()
+    lib = fca.load_library()
+    k, v, slots, kc, vc = (i << 24 for i in range(1, 6))
+    #       k  stride v  stride slots T NB Hkv D kc vc status stream; a cache has 8 * 16 * 256 bytes
+    good = [k, 384, v, 384, slots, 3, 8, 2, 64, kc, vc, None, None]
+    for at, where in ((10, kc), (10, kc + 32752), (9, k + 1536 + 240), (10, k), (9, v + 16), (10, slots), (9, slots - 32752)):
+        a = list(good)
+        a[at] = where
+        assert lib.fca_append_kv(*a) == 1, (at, where)

@@ -764,3 +764,22 @@ def test_two_plans_at_once():
     for x, p in zip(b, plans):
         check(x, what="two plans")
         p.close()
+
+
+def test_attention_in_place_is_refused():
+    torch = _torch()
+    import shared_prefix_kv_fca_b200 as fca
+    b = Batch([40, 17], [3, 17], 8, 2, 64, seed=23, packed=False)
+    with b.plan() as plan:
+        flat = torch.zeros(b.T * b.hq * b.d + 8, dtype=torch.bfloat16, device="cuda")
+        for out in (b.q, flat[:-8].view(b.q.shape)):
+            q = b.q if out is b.q else flat[8:].view(b.q.shape)
+            before = q.clone()
+            with pytest.raises(fca.FcaError, match="INVALID_ARG"):
+                fca.fca_chunk_attention(q, b.k, b.v, plan, out, b.lse, b.scale)
+            assert torch.equal(q, before)
+        lse = flat[:b.T * b.hq * 2].view(torch.float32).view(b.T, b.hq)
+        with pytest.raises(fca.FcaError, match="INVALID_ARG"):
+            fca.fca_chunk_attention(b.q, b.k, b.v, plan, flat[:-8].view(b.q.shape), lse, b.scale)
+        b.attend(plan)
+        check(b, what="after refusals")
