@@ -110,8 +110,8 @@ struct Layout {
     static constexpr int kOffQ = 0;                      // two tiles
     static constexpr int kOffK = kOffQ + 2 * kTileQ;
     static constexpr int kOffV = kOffK + kKSlots * kKV;
-    static constexpr int kOffML = kOffV + kVSlots * kKV; // [2][128] f32: tile 1's row references and sums, for tile 0
-    static constexpr int kOffBar = kOffML + 2 * 128 * 4;
+    static constexpr int kOffML = kOffV + kVSlots * kKV; // [3][128] f32: tile 1's row references and sums, for tile 0
+    static constexpr int kOffBar = kOffML + 3 * 128 * 4;
     static constexpr int kNumBars = 2 * (kKSlots + kVSlots) + 5 * 2 + 4;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
     static constexpr int kAlloc = kOffMisc + 32;
@@ -217,7 +217,7 @@ __device__ __forceinline__ void max32(const uint32_t (&x)[32], float& a, float& 
 }
 
 // Weights of 32 scores against the reference (nm = -m): 16 bf16 pairs, and their sum
-// before rounding.
+// before rounding (for lse).
 __device__ __forceinline__ void weights32(const uint32_t (&x)[32], float2 sc, float2 nm, uint32_t* p, float2& sum) {
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
@@ -226,6 +226,22 @@ __device__ __forceinline__ void weights32(const uint32_t (&x)[32], float2 sc, fl
         p[i / 2] = dev::pack_bf16x2(e.x, e.y);
         sum = dev::add2(sum, e);
     }
+}
+
+// The sum of 64 weights as they were rounded, which is what P V applies: out divided by it stays a
+// weighted mean of V.  (Divided by the sum before rounding, a row whose weight sits on one token
+// would be off by that weight's rounding, up to 2^-8, in all elements at once.)  Taken behind the
+// weights' hand-over, while the tile waits for its next scores, by adds that read a bf16 as it
+// lies: 16 prompts of 2048 take 632 us, 603 without this sum, 640 with it among the exponentials,
+// 652 with pairs unpacked and added two at a time, 723 with warp products.
+__device__ __forceinline__ float rounded_sum(const uint32_t (&p)[32]) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        dev::add_bf16x2(s[0], s[1], p[i]);
+        dev::add_bf16x2(s[2], s[3], p[i + 1]);
+    }
+    return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 // Whether V has an inf or NaN in tokens [tok0, tok1), by one warp.
@@ -477,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int32_t all = max(0, __reduce_min_sync(0xffffffffu, lim)) / kStage;
                 n_hot = min(ns, w.dual ? (all - t + 1) >> 1 : all);
             }
-            float m = -INFINITY, l = 0.f;       // reference (log2 domain) and sum of the weights
+            float m = -INFINITY, l = 0.f, lr = 0.f;     // reference (log2 domain), sums of the weights and of the rounded ones
             // Before a stage's first weights: the P V of the tile's stage before has read
             // the last ones.
             auto weights_free = [&]() -> bool {
@@ -532,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (mx > m + kRescaleLog2) {
                     f = dev::ex2(m - mx);
                     l *= f;
+                    lr *= f;
                     m = mx;
                 }
                 // (an item's first P V overwrites the accumulator)
@@ -553,19 +570,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float m0 = m == -INFINITY ? 0.f : m;       // nothing seen yet: every weight is 2^-inf
                 const float2 sc = make_float2(a.scale_log2, a.scale_log2), nm = make_float2(-m0, -m0);
                 float2 sum = make_float2(0.f, 0.f), sum2 = make_float2(0.f, 0.f);
-                uint32_t p[32];
+                uint32_t p[32], p2[32];
                 weights32(s0, sc, nm, p, sum);
                 weights32(s1, sc, nm, p + 16, sum2);
                 if (!weights_free()) return false;
                 dev::tmem_st32(p_addr, p);
-                weights32(s2, sc, nm, p, sum);
-                weights32(s3, sc, nm, p + 16, sum2);
-                dev::tmem_st32(p_addr + 32, p);
+                weights32(s2, sc, nm, p2, sum);
+                weights32(s3, sc, nm, p2 + 16, sum2);
+                dev::tmem_st32(p_addr + 32, p2);
                 sum = dev::add2(sum, sum2);
                 l += sum.x + sum.y;
                 dev::tc_wait_st();
                 dev::tc_fence_before();
                 dev::mbar_arrive(&p_full[t]);
+                lr += rounded_sum(p) + rounded_sum(p2);      // while the tile waits for its next scores
                 return true;
             };
             int32_t x = 0;
@@ -604,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (join) {
                     ml[row] = m;
                     ml[128 + row] = l;
+                    ml[256 + row] = lr;
                     dev::mbar_arrive(x_full);
                     ok = __all_sync(0xffffffffu, dev::mbar_wait(x_free, n_dual & 1, abort_flag, a.err));
                     ++n_dual;
@@ -617,19 +636,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             float c0, c1 = 0.f, lw;             // coefficients of the accumulators; the row's log2 sum
             {
                 bool up = ns == 0 || dev::mbar_wait(&pv_done[t], (g - 1) & 1, abort_flag, a.err);
-                float m1 = -INFINITY, l1 = 0.f;
+                float m1 = -INFINITY, l1 = 0.f, lr1 = 0.f;
                 if (join) {
                     up = up && dev::mbar_wait(x_full, n_dual & 1, abort_flag, a.err) &&
                          dev::mbar_wait(&pv_done[1], (g_other - 1) & 1, abort_flag, a.err);
                     m1 = ml[row];
                     l1 = ml[128 + row];
+                    lr1 = ml[256 + row];
                     ++n_dual;
                 }
                 if (!__all_sync(0xffffffffu, up)) { ok = false; break; }
                 dev::tc_fence_after();
                 const float M = fmaxf(m, m1), Mf = M == -INFINITY ? 0.f : M;
                 const float f0 = dev::ex2(m - Mf), f1 = dev::ex2(m1 - Mf);
-                const float sum = l * f0 + l1 * f1, inv = sum == 0.f ? 0.f : 1.f / sum;
+                const float sum = l * f0 + l1 * f1, sum_r = lr * f0 + lr1 * f1, inv = sum_r == 0.f ? 0.f : 1.f / sum_r;
                 c0 = f0 * inv;
                 c1 = f1 * inv;
                 lw = M + log2f(sum);            // -inf for a row that saw nothing

@@ -310,6 +310,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return r;
 }
 
+// a += the lower, b += the upper bf16 of v (sm_100: fp32 + bf16 in one instruction).  Not
+// moved ahead of other volatile statements.
+__device__ __forceinline__ void add_bf16x2(float& a, float& b, uint32_t v) {
+    uint16_t lo, hi;
+    asm volatile("mov.b32 {%0, %1}, %2;" : "=h"(lo), "=h"(hi) : "r"(v));
+    asm("add.rn.f32.bf16 %0, %1, %0;" : "+f"(a) : "h"(lo));
+    asm("add.rn.f32.bf16 %0, %1, %0;" : "+f"(b) : "h"(hi));
+}
+
 // Shared-memory matrix descriptor, 128-byte swizzle, sm_100 version bits.
 // lbo/sbo in bytes.
 __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
