@@ -190,6 +190,14 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// mbar_wait by a warp whose lanes go on together.  When a wait is given up (its limit, or the
+// abort flag) just as the phase completes, lanes may come back with different answers: all of
+// them leave then, since one that went on alone would wait for the others in the next vote,
+// without a limit.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* err_word) {
+    return __all_sync(0xffffffffu, dev::mbar_wait(bar, parity, abort, err_word));
+}
+
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -454,9 +462,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (; i < last; ++i) {
                 const Work w = load_work(a, i);
                 if (t ? w.dual || w.ns == 0 : w.ns0 == 0) continue;
-                if (n_q && !dev::mbar_wait(&q_free[t], (n_q - 1) & 1, abort_flag, a.err)) ok = false;
-                ++n_q;
+                if (n_q) ok = warp_wait(&q_free[t], (n_q - 1) & 1, abort_flag, a.err);
                 if (!ok) return;
+                ++n_q;
                 constexpr int C = D / 8;            // 16-byte chunks a row
                 const uint32_t q_tile = dev::smem_u32(smem + L::kOffQ) + t * L::kTileQ;
 #pragma unroll 4
@@ -497,9 +505,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Before a stage's first weights: the P V of the tile's stage before has read
             // the last ones.
             auto weights_free = [&]() -> bool {
-                const bool up = g == 0 || dev::mbar_wait(&pv_done[t], (g - 1) & 1, abort_flag, a.err);
+                const bool up = g == 0 || warp_wait(&pv_done[t], (g - 1) & 1, abort_flag, a.err);
                 dev::tc_fence_after();
-                return __all_sync(0xffffffffu, up);
+                return up;
             };
             // Stage x.  In an edge stage (x >= n_hot) some row of the warp does not see all
             // 128 columns: those are set to -inf where they lie first, in a short loop, so that
@@ -507,8 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // an item come from far: a second body with masks cost 3500 cycles an item).
             auto stage = [&](int32_t x) -> bool {
                 const int32_t j = dual ? 2 * x + t : x;
-                bool got = dev::mbar_wait(&s_full[t], g & 1, abort_flag, a.err);
-                if (!__all_sync(0xffffffffu, got)) return false;
+                if (!warp_wait(&s_full[t], g & 1, abort_flag, a.err)) return false;
                 dev::tc_fence_after();
                 if (x >= n_hot) {
                     const int nv = lim - j * kStage;             // columns that the row sees
@@ -594,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // rows that do not exist: the barriers only
 #pragma unroll 1
                 for (; ok && x < ns; ++x, ++g) {
-                    ok = __all_sync(0xffffffffu, dev::mbar_wait(&s_full[t], g & 1, abort_flag, a.err));
+                    ok = warp_wait(&s_full[t], g & 1, abort_flag, a.err);
                     if (!ok) break;
                     dev::mbar_arrive(s_free);
                     ok = weights_free();
@@ -624,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ml[128 + row] = l;
                     ml[256 + row] = lr;
                     dev::mbar_arrive(x_full);
-                    ok = __all_sync(0xffffffffu, dev::mbar_wait(x_free, n_dual & 1, abort_flag, a.err));
+                    ok = warp_wait(x_free, n_dual & 1, abort_flag, a.err);
                     ++n_dual;
                 }
                 continue;
@@ -635,17 +642,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool mine = r_item < w.it.nrows;
             float c0, c1 = 0.f, lw;             // coefficients of the accumulators; the row's log2 sum
             {
-                bool up = ns == 0 || dev::mbar_wait(&pv_done[t], (g - 1) & 1, abort_flag, a.err);
+                bool up = ns == 0 || warp_wait(&pv_done[t], (g - 1) & 1, abort_flag, a.err);
                 float m1 = -INFINITY, l1 = 0.f, lr1 = 0.f;
                 if (join) {
-                    up = up && dev::mbar_wait(x_full, n_dual & 1, abort_flag, a.err) &&
-                         dev::mbar_wait(&pv_done[1], (g_other - 1) & 1, abort_flag, a.err);
+                    up = up && warp_wait(x_full, n_dual & 1, abort_flag, a.err) &&
+                         warp_wait(&pv_done[1], (g_other - 1) & 1, abort_flag, a.err);
                     m1 = ml[row];
                     l1 = ml[128 + row];
                     lr1 = ml[256 + row];
                     ++n_dual;
                 }
-                if (!__all_sync(0xffffffffu, up)) { ok = false; break; }
+                if (!up) { ok = false; break; }
                 dev::tc_fence_after();
                 const float M = fmaxf(m, m1), Mf = M == -INFINITY ? 0.f : M;
                 const float f0 = dev::ex2(m - Mf), f1 = dev::ex2(m1 - Mf);
@@ -819,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // registers; one elected thread issues.
             bool ok = true;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
-                if (ok) ok = __all_sync(0xffffffffu, dev::mbar_wait(bar, parity, abort_flag, a.err));
+                if (ok) ok = warp_wait(bar, parity, abort_flag, a.err);
                 return ok;
             };
             uint32_t g = 0;                     // stages of the CTA before the item
