@@ -267,10 +267,9 @@ __device__ __noinline__ bool v_not_finite(const ChunkArgs& a, int32_t req, int32
 
 // Rows row0 + i of item `item`, for the bits i of `rows`, by one warp with plain arithmetic, from the
 // tokens that they see; the results are written over what is there.  Does nothing where V is finite
-// in all that some of them do not see: then they are what they should be.  Other roles
-// wait meanwhile, no longer than their limit, so rows are taken kExactRows at a time and tokens 32
-// at a time, a lane a token for the scores: 64 rows of 30000 tokens on every SM at once
-// take 48 ms (512 ms a row at a time).
+// in all that some of them do not see: then they are what they should be.  Rows are taken
+// kExactRows at a time and tokens 32 at a time, a lane a token for the scores: 256 stacked rows of 30000
+// tokens on every SM at once take 48 ms (512 ms a row at a time).
 constexpr int kExactRows = 8;
 
 template <int D>
@@ -381,6 +380,37 @@ __device__ __noinline__ void exact_rows(const ChunkArgs& a, int32_t item, int ro
     }
 }
 
+// Whether a lane's row, as it was stored, has an inf or NaN.
+template <int D>
+__device__ __forceinline__ bool not_finite(const ChunkArgs& a, const ChunkItem& it, int32_t row) {
+    bool bad = false;
+    if (it.slot < 0) {
+        int32_t qhead;
+        const int32_t tok = row_token(a, it, row, qhead);
+        const __nv_bfloat16* const p = a.out + ((int64_t)tok * a.Hq + qhead) * D;
+#pragma unroll 8
+        for (int e = 0; e < D; ++e) bad |= !(fabsf(__bfloat162float(p[e])) < INFINITY);
+    } else {
+        const float* const p = a.part_o + ((int64_t)it.slot * a.part_rows + row) * D;
+#pragma unroll 8
+        for (int e = 0; e < D; ++e) bad |= !(fabsf(p[e]) < INFINITY);
+    }
+    return bad;
+}
+
+// The rows that are not finite among a warp's rows row0 + lane of all the CTA's items.  A warp comes here
+// behind its last item, when it has arrived at every barrier that others wait for: however long it
+// takes, no wait with a limit runs meanwhile.
+template <int D>
+__device__ __noinline__ void exact_items(const ChunkArgs& a, int32_t first, int32_t last, int row0) {
+    for (int32_t i = first; i < last; ++i) {
+        const ChunkItem it = load_work(a, i).it;
+        const int r = row0 + (threadIdx.x & 31);
+        const uint32_t again = __ballot_sync(0xffffffffu, r < it.nrows && not_finite<D>(a, it, r));
+        if (again) exact_rows<D>(a, i, row0, again);
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     k_chunk(const __grid_constant__ ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
@@ -452,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         const uint32_t s_addr = tmem + lane_base + L::kColS, p_addr = tmem + lane_base + L::kColP + t * 64,
                        o_addr = tmem + lane_base + L::kColO + t * D;
-        bool ok = true;
+        bool ok = true, redo = false;
         // Where the head group does not divide a tile (else the V warp loads the queries by TMA):
         // queries of tile t for the next item that has some, from item i on (a dual item's go to
         // tile 0), once the products reading the last ones have completed.
@@ -722,9 +752,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // A product of weight 0 with an inf or NaN that the row does not see
             // (a later token's) is NaN: a row that is not finite is computed again from
             // the tokens that it does see, if V is not finite in one that it does not.
-            const uint32_t again = __ballot_sync(0xffffffffu, mine && isnan(finite));
-            if (again) exact_rows<D>(a, i, t * 128 + quarter * 32, again);
+            redo |= mine && isnan(finite);
         }
+        if (ok && __any_sync(0xffffffffu, redo)) exact_items<D>(a, first, last, warp * 32);
     } else {
         regs_dec<kRegsOthers>();
         if (warp == kKWarp || warp == kVWarp) {
