@@ -1061,9 +1061,9 @@ extern "C" fca_status fca_chunk_attention(const void* q, int64_t q_row_stride, c
     const size_t n_out = heads * plan->D * 2, n_lse = lse ? heads * 4 : 0;
     const size_t n_q = ((rows - 1) * q_row_stride + (size_t)plan->Hq * plan->D) * 2;
     if (overlap(out, n_out, lse, n_lse)) return FCA_ERR_INVALID_ARG;
-    for (const void* in : {q, k_cache, v_cache})
-        if (overlap(in, in == q ? n_q : cache, out, n_out) || overlap(in, in == q ? n_q : cache, lse, n_lse))
-            return FCA_ERR_INVALID_ARG;
+    const struct { const void* at; size_t bytes; } in[3] = {{q, n_q}, {k_cache, cache}, {v_cache, cache}};
+    for (const auto& x : in)
+        if (overlap(x.at, x.bytes, out, n_out) || overlap(x.at, x.bytes, lse, n_lse)) return FCA_ERR_INVALID_ARG;
     DeviceGuard dg(plan->device);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CUtensorMap tk, tv;
