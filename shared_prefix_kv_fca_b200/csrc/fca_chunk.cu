@@ -513,7 +513,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         load_q(first);
         uint32_t g = 0, g_other = 0;    // stages of this tile, and of the other, before the item
-        uint32_t gv = 0;                // stages of the CTA before the item
         uint32_t n_dual = 0;            // items joined from both tiles
         for (int32_t i = first; ok && i < last; ++i) {
             int32_t ns, ns_other, ns_item, lim, n_hot;
@@ -649,7 +648,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok) break;
-            gv += ns_item;
             g_other += ns_other;
             if (ns && (t == 0 || !dual)) load_q(i + 1);
             if (!ok) break;
