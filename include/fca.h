@@ -361,6 +361,9 @@ fca_status fca_paged_decode_static(const void *q, const void *k_cache, const voi
  * and brings new_lens[r]; the new tokens of all requests are packed in
  * request order, request r's in rows [q_starts[r], q_starts[r + 1]).
  * Error bits that the kernels OR into a device status word:
+ *   1    a wait inside the attention kernel gave up after a second: a fault, not
+ *        an input; what the call was to write is undefined
+ *   2    the attention kernel found its shared memory misplaced and wrote nothing
  *   8    a length, or a request's range of rows, is out of range
  *   16   a used block id or slot is out of range
  *   64   the free list has too few blocks
@@ -402,8 +405,9 @@ fca_status fca_paged_decode_static(const void *q, const void *k_cache, const voi
  * the calls that follow have no new tokens.
  *
  * Returns FCA_ERR_INVALID_ARG (null or misaligned pointer, bad shape, an output
- * that overlaps another buffer otherwise than stated), FCA_ERR_UNSUPPORTED (over 16384 requests or 2^30 slots, or
- * num_blocks or max_blocks beyond 2^31 / 16), FCA_ERR_CUDA.  num_requests == 0
+ * that overlaps another buffer otherwise than stated), FCA_ERR_UNSUPPORTED (over
+ * 16384 requests or 2^30 slots, or num_blocks or max_blocks beyond 2^31 / 16),
+ * FCA_ERR_CUDA.  num_requests == 0
  * sets q_starts[0] to 0, the slots to -1 and free_after.  Asynchronous on
  * `stream`, one kernel or two, no workspace; runs on the current device.
  */
@@ -492,8 +496,12 @@ fca_status fca_chunk_plan_update(fca_chunk_plan_t plan, const int32_t *block_tab
  * fca_chunk_attention -- softmax attention of the plan's rows over the paged
  * cache, one layer.  Row i of a request with n rows and seq_len L is at
  * position p = L - n + i and sees tokens 0..p (with FCA_CHUNK_FULL: all L).  What a
- * row does not see has no part in it, whatever it holds (inf and NaN included).
- * A row that sees nothing gets out 0 and lse -inf.
+ * row does not see has no part in it, whatever it holds (inf and NaN included):
+ * rows beside values that are not finite are computed again by plain arithmetic,
+ * which is slow (256 rows x query heads of one KV head over 1.6 million tokens:
+ * 2 s) but has no limit.  A row that sees nothing gets out 0 and lse -inf.
+ * The weights that multiply V are rounded to bf16, and out is divided by the
+ * sum of the rounded ones: it is a weighted mean of the values that the row sees.
  *
  *   q        DEVICE bf16, num_tokens rows of [num_q_heads][head_dim], 16-byte
  *            aligned, q_row_stride elements apart (a multiple of 8, at least

@@ -24,7 +24,9 @@
 //                each stage they read the scores from tensor memory into
 //                registers and write the weights back as bf16; the accumulator is
 //                rescaled in place in the rare case that a row's maximum
-//                outgrows its reference; at the item's end they normalise and store;
+//                outgrows its reference; at the item's end they normalise and store.
+//                Two row sums: of the rounded weights, by which out is divided, and
+//                of those before rounding, for lse;
 //   warps 8, 9   TMA loads of K, and of V and the queries; one block of 16
 //                tokens, or 16 stacked query rows, a box;
 //   warps 10, 11 MMA issue: S = Q K^T (operands in shared memory), and
@@ -35,19 +37,20 @@
 // anything, so that the other tile's Q K^T, and this tile's next, never wait for an
 // exponential or a P V.  (With a score buffer per tile and the weights
 // written over the scores, a tile's next Q K^T had to wait for its P V:
-// 5300 cycles a stage of 256 x 128 instead of 3300.)
+// 5300 cycles a stage of 256 x 128 instead of then 3300.)
 //
 // What bounds it.  A stage of 256 x 128 at head_dim 128 needs 2048 tensor cycles,
 // 2048 cycles of exponentials (16 a cycle and SM) and 2048 of shared-memory reads,
-// and takes 3300: the softmax of the two tiles, two warps a scheduler, takes 2350
-// by itself, and what the tiles wait for each other does the rest.  Measured: 4096 tokens
-// behind 32768 (32/8/128) 1.9 ms, 1230 TFLOP/s (74% of the measured burst rate; 2.2 ms in
-// runs of seconds, at the clock that power leaves); 16 prompts of 2048 600 us,
-// 920 TFLOP/s: an item's start and end cost 3.5 us.  Dual items are
-// bound by the cache's bytes: 192 x 5 drafted tokens (3.8 GB) 6.5 TB/s, 99% of the copy
-// rate; 64 x 5 (0.85 GB) 5.3 TB/s, with 15 us of start and end.  Tried and slower: exponentials partly by a polynomial on the FMA
-// pipe; 16 softmax warps of 64 columns; one warp issuing both products in
-// order; a second score buffer at head_dim 64; P handed over in halves.
+// and takes 3400 (3300 without the sum of rounded weights): the softmax of the two
+// tiles, two warps a scheduler, takes 2350 by itself without that sum.  Where the rest goes
+// is not known in full; a second score buffer, which head_dim 64 has room for, gained
+// nothing.  Measured: 4096 tokens behind 32768 (32/8/128) 1.99 ms, 1175 TFLOP/s (71% of the
+// measured burst rate; 2.37 ms in runs of seconds, at the clock that power leaves); 16 prompts
+// of 2048 630 us, 872 TFLOP/s: an item's start and end cost 3.5 us.  Dual items are
+// bound by the cache's bytes: 192 x 5 drafted tokens behind 1500-8000 (3.8 GB) 6.4 TB/s, 98% of
+// the copy rate; 64 x 5, of which 1024 shared (0.85 GB), 5.2 TB/s, with 15 us of start and
+// end.  Tried and slower: exponentials partly by a polynomial on the FMA pipe; 16 softmax
+// warps of 64 columns; one warp issuing both products in order; P handed over in halves.
 //
 // Every wait is bounded (fca_device.cuh); a role that gives up sets the CTA's
 // abort flag, the others leave at their next wait, copies and MMAs in flight

@@ -15,7 +15,8 @@ constexpr int kChunkStage = 128;     // tokens a pipeline stage
 // What a stage and a tile itself (query load, pipeline fill, last P V, storing) cost, in
 // units of about 0.25 us: tiles above 128 rows are bound by the softmax and the products, the
 // others by the cache's bytes.  A chunk of 1999 tokens (64/8/128) beside 95 decodes takes
-// 555 us with equal costs for all stages, 526 us at 4 : 3, 515 us at 8 : 5 and 580 us at 2 : 1.
+// 555 us with equal costs for all stages, 526 us at 4 : 3, 515 us at 8 : 5 and 580 us at 2 : 1
+// (head_dim 128, before a second row sum that costs 3% of it; not tried at head_dim 64).
 constexpr int kChunkStageCost = 8, kChunkTileCost = 14;
 constexpr int kChunkHalfStageCost = 5, kChunkHalfTileCost = 10;
 constexpr int kChunkMinPiece = 2;    // fewest stages a tile is cut into
